@@ -1,0 +1,86 @@
+"""MXFP4 operators without a GPU: the C ABI refuses bad arguments before any
+device work, the binding refuses tensors it does not take, and the 64-bit
+reference that the GPU tests compare with has the format's properties."""
+import numpy as np
+import pytest
+import torch
+
+from sigmoid_bias_top_b200 import mx
+from tests import mx_ref as R
+
+
+def test_quantize_refusals():
+    L = mx.lib()
+
+    def call(x=256, dtype=1, rows=4, K=64, ld=64, codes=256, scales=256):
+        return L.moe_mx_quantize(x, dtype, rows, K, ld, codes, scales, None)
+    assert call(dtype=2) == -1 and call(rows=-1) == -1 and call(x=None) == -1
+    assert call(codes=None) == -1 and call(scales=None) == -1
+    assert call(K=48) == -2 and call(K=0) == -2 and call(K=-32) == -2
+    assert call(rows=1 << 60) == -2
+    assert call(ld=32) == -1                        # rows would overlap
+    assert call(ld=65) == -3                        # bf16 rows off 16 bytes
+    assert call(dtype=0, ld=66) == -3
+    assert call(x=264) == -3 and call(codes=264) == -3 and call(scales=258) == -3
+    assert call(rows=0, x=None, codes=None, scales=None) == 0
+
+
+def test_dequantize_refusals():
+    L = mx.lib()
+
+    def call(codes=256, scales=256, rows=4, K=64, y=256, dtype=1):
+        return L.moe_mx_dequantize(codes, scales, rows, K, y, dtype, None)
+    assert call(dtype=2) == -1 and call(rows=-1) == -1 and call(y=None) == -1
+    assert call(K=33) == -2
+    assert call(y=260) == -3 and call(codes=8) == -3 and call(scales=6) == -3
+    assert call(rows=0) == 0
+
+
+def test_matmul_refusals():
+    L = mx.lib()
+
+    def call(a=256, a_s=256, w=256, w_s=256, offs=256, rows=4, K=256, E=2, N=64, silu=0, out=256,
+             dtype=1):
+        return L.moe_mx_matmul(a, a_s, w, w_s, offs, rows, K, E, N, silu, out, dtype, None)
+    assert call(dtype=2) == -1 and call(rows=-1) == -1 and call(silu=2) == -1
+    assert call(offs=None) == -1                    # two experts need offsets
+    for name in ("a", "a_s", "w", "w_s", "out"):
+        assert call(**{name: None}) == -1, name
+    assert call(K=64) == -2 and call(K=0) == -2 and call(N=0) == -2 and call(N=24) == -2
+    assert call(N=48, silu=1) == -2 and call(E=0) == -2 and call(E=257) == -2
+    assert call(rows=1 << 30) == -2 and call(E=256, N=1 << 22) == -2
+    assert call(a=264) == -3 and call(w=264) == -3 and call(out=264) == -3
+    assert call(a_s=258) == -3 and call(w_s=258) == -3 and call(offs=258) == -3
+    assert call(rows=0, a=None, out=None) == 0
+
+
+def test_binding_refuses_other_tensors():
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        mx.quantize(x)                               # not on a GPU
+    with pytest.raises(TypeError):
+        mx.quantize(x.half())
+    q = mx.MxTensor(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        mx.dequantize(q)
+    with pytest.raises(TypeError):
+        mx.matmul(q, q)
+    with pytest.raises(TypeError):
+        mx.dequantize(q, torch.float16)
+    assert q.shape == (4, 64)
+
+
+def test_reference_rounding():
+    """Ties go to the even code, values above 6 saturate, the exponent follows
+    the block's largest value."""
+    x = np.zeros((1, 32))
+    x[0, :16] = [4, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -0.25, -0.76, -5.01, 7.9, 0.26, 0, 6, 1]
+    codes, scales = R.quantize(x)
+    assert scales[0, 0] == 127
+    v = R.values(codes, scales)[0, :16]
+    assert v.tolist() == [4, 0, 1, 1, 2, 2, 4, 4, -0.0, -1, -6, 6, 0.5, 0, 6, 1]
+    y = np.full((1, 32), np.nan)
+    assert R.quantize(y)[1][0, 0] == 255
+    assert R.quantize(np.full((1, 32), 2.0 ** -149))[1][0, 0] == 0
+    z, s = R.quantize(np.zeros((1, 32)))
+    assert s[0, 0] == 0 and not z.any()
