@@ -1,0 +1,123 @@
+"""ctypes binding of the router's balance loss (include/balance.h): argument
+checks, autograd and marshalling only; the loss, the counts and the gradient
+are computed by libmoe.so's CUDA kernels.
+
+For router logits l [n, E] and the selected experts idx [n, k] (route_noalloc),
+in the sequences b that seq_offsets cuts the tokens into, T_b tokens each:
+  s = sigmoid(l),  p_te = s_te / (sum_j s_tj + eps)
+  f_be = E counts_be / (k T_b),  prob_be = mean over b's tokens of p_te
+  loss = coef * mean over the sequences with tokens of sum_e f_be prob_be
+The counts carry no gradient; that of the logits runs through p.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import MOE_BF16, MOE_F32, _check, lib as _moe_lib
+from .mx import _On
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+class Balance(NamedTuple):
+    loss: torch.Tensor     # [] f32, differentiable with respect to the logits
+    counts: torch.Tensor   # [B, E] int32: slots of the sequence's tokens that hold the expert
+    prob: torch.Tensor     # [B, E] f32: mean normalised score (no gradient)
+
+
+_bound = False
+
+
+def lib():
+    global _bound
+    L = _moe_lib()
+    if not _bound:
+        P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+        L.moe_balance_workspace.argtypes = [I, I, I]
+        L.moe_balance_workspace.restype = ctypes.c_size_t
+        L.moe_balance_forward.argtypes = [P, I, I64, P, P, I, I, I, I, F, F, P, P, P, P, P, P]
+        L.moe_balance_forward.restype = I
+        L.moe_balance_backward.argtypes = [P, I, I64, P, P, P, P, I, I, I, I, F, P, P]
+        L.moe_balance_backward.restype = I
+        _bound = True
+    return L
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ld(logits):
+    """Elements from a row to the next (any, where there is no next)."""
+    return logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, idx, seq_offsets, coef, eps):
+        n, E = logits.shape
+        k, dev = idx.shape[1], logits.device
+        B = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        L = lib()
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        scale = torch.empty((), dtype=torch.float32, device=dev)
+        counts = torch.empty(B, E, dtype=torch.int32, device=dev)
+        prob = torch.empty(B, E, dtype=torch.float32, device=dev)
+        with _On(dev, None) as s:
+            ws = torch.empty(L.moe_balance_workspace(n, E, B), dtype=torch.uint8, device=dev)
+            _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype],
+                                         _ld(logits), idx.data_ptr(), _ptr(seq_offsets), n, E,
+                                         k, B, coef, eps, ws.data_ptr(), loss.data_ptr(),
+                                         counts.data_ptr(), prob.data_ptr(), scale.data_ptr(), s),
+                   "moe_balance_forward")
+        ctx.save_for_backward(logits, counts, scale, seq_offsets)
+        ctx.k, ctx.eps = k, eps
+        ctx.mark_non_differentiable(counts, prob)
+        return loss, counts, prob
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss, _counts, _prob):
+        logits, counts, scale, seq_offsets = ctx.saved_tensors
+        n, E = logits.shape
+        grad = torch.empty(n, E, dtype=logits.dtype, device=logits.device)
+        grad_loss = grad_loss.float()
+        with _On(logits.device, None) as s:
+            _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype],
+                                              _ld(logits), counts.data_ptr(),
+                                              _ptr(seq_offsets), scale.data_ptr(),
+                                              grad_loss.data_ptr(), n, E, ctx.k, counts.shape[0],
+                                              ctx.eps, grad.data_ptr(), s),
+                   "moe_balance_backward")
+        return grad, None, None, None, None
+
+
+def balance_loss(logits, idx, seq_offsets: Optional[torch.Tensor] = None, coef: float = 1.0,
+                 eps: float = 1e-6) -> Balance:
+    """Balance loss, per-expert counts and mean scores of a routed batch.
+
+    logits [n, E] f32 or bf16 (rows may be strided), idx [n, k] int32 (values
+    outside [0, E) are dropped slots and not counted), seq_offsets [B + 1] int32
+    on the device (None: one sequence of all tokens); tokens of no sequence take
+    no part and get a zero gradient. Runs on the current stream; the backward pass
+    on the stream that autograd gives it. E <= 256, k <= min(E, 8)."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES:
+        raise TypeError("logits must be a float32 or bfloat16 tensor")
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be an [n, E] CUDA tensor")
+    n, E = logits.shape
+    if E > 1 and logits.stride(1) != 1 or _ld(logits) < E:
+        logits = logits.contiguous()
+    if (idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != n
+            or not idx.is_contiguous() or idx.device != logits.device):
+        raise ValueError(f"idx must be a contiguous int32 ({n}, k) tensor on {logits.device}")
+    if seq_offsets is not None and (
+            seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 2
+            or not seq_offsets.is_contiguous() or seq_offsets.device != logits.device):
+        raise ValueError("seq_offsets must be a contiguous int32 (B + 1,) tensor on "
+                         f"{logits.device}")
+    return Balance(*_BalanceLoss.apply(logits, idx, seq_offsets, float(coef), float(eps)))
