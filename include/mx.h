@@ -64,6 +64,11 @@ int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t
                   const uint8_t *w_scales, const int32_t *offsets, int rows, int K, int n_experts,
                   int N, int silu_mul, void *out, int dtype, void *stream);
 
+/* moe_mx_matmul waits inside its kernel with a limit of a second. Waits for the
+ * device, then reads and clears what the calls on it since the last reading
+ * met: MOE_OK or MOE_ERR_DEVICE_TIMEOUT (out of that call is then incomplete). */
+int moe_mx_status(void);
+
 #ifdef __cplusplus
 }
 #endif

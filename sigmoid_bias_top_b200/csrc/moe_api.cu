@@ -21,8 +21,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <map>
 #include <mutex>
-#include <unordered_map>
 #include <vector>
 
 #include "moe_fp8.cuh"
@@ -89,10 +89,12 @@ static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 int moe::ensure_smem_ptr(const void *kern, size_t smem) {
     static std::mutex mu;
-    static std::unordered_map<const void *, size_t> set;  // per process (one device each)
+    static std::map<std::pair<int, const void *>, size_t> set;  // the limit is a device's own
     if (smem <= 48 * 1024) return MOE_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mu);
-    size_t &cur = set[kern];
+    size_t &cur = set[{dev, kern}];
     if (smem <= cur) return MOE_OK;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(smem));

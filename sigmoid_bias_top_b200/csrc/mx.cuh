@@ -21,7 +21,7 @@ struct MxMatmulParams {
 
 int launch_mx_quantize(const void *x, int dtype, int64_t rows, int K, int64_t ld, uint8_t *codes,
                        uint8_t *scales, cudaStream_t s);
-int launch_mx_matmul(const MxMatmulParams &p, cudaStream_t s);
+int launch_mx_matmul(const MxMatmulParams &p, int n_sm, cudaStream_t s);
 
 // The value of an E8M0 scale (2^-127 is an fp32 subnormal; 255 is NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t s) {

@@ -41,7 +41,9 @@ def lib():
         L.moe_mx_quantize.argtypes = [P, I, I64, I, I64, P, P, P]
         L.moe_mx_dequantize.argtypes = [P, P, I64, I, P, I, P]
         L.moe_mx_matmul.argtypes = [P, P, P, P, P, I, I, I, I, I, P, I, P]
-        for f in (L.moe_mx_quantize, L.moe_mx_dequantize, L.moe_mx_matmul):
+        L.moe_mx_status.argtypes = []
+        for f in (L.moe_mx_quantize, L.moe_mx_dequantize, L.moe_mx_matmul,
+                  L.moe_mx_status):
             f.restype = I
         _bound = True
     return L
@@ -173,3 +175,10 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
                                    int(silu_mul), out.data_ptr(), _DTYPES[dtype], s),
                "moe_mx_matmul")
     return out
+
+
+def status(device=None) -> int:
+    """Waits for the device; 0, or the code of a time-out inside a matmul on it
+    since the last call (whose result is then incomplete)."""
+    with torch.cuda.device(device):
+        return lib().moe_mx_status()
