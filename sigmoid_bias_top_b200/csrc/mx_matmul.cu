@@ -19,8 +19,8 @@
 // on to TMEM (tcgen05.cp) before the stage's four MMAs. Every stage has TMEM
 // columns of its own for them: a stage is refilled only after its MMAs have
 // completed, so nothing is overwritten early.
-// Roles (384 threads): warp 0 lane 0 issues TMA, warp 1 lane 0 copies scales
-// and issues MMAs, warps 2 and 3 load the scales of the weights and of the
+// Roles (384 threads): a thread of warp 0 issues TMA, one of warp 1 copies
+// scales and issues MMAs, warps 2 and 3 load the scales of the weights and of the
 // rows, warps 4..11 drain the accumulators (two in TMEM, so that a tile's
 // epilogue runs under the next tile's MMAs). Items (expert, weight tile, row
 // tile) are dealt out in a fixed order; every CTA forms the plan from the
@@ -76,6 +76,21 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Ctl *ct
 
 __device__ __forceinline__ bool aborted(Ctl *ctl) {
     return *reinterpret_cast<volatile int *>(&ctl->abort) != 0;
+}
+
+// True in one lane of the (converged) warp. The compiler knows that a region
+// under it runs in a single thread and feeds the tcgen05 and TMA instructions'
+// operands through uniform registers directly; under a test of the lane index
+// every such instruction costs about 70 cycles to issue, which at four MMAs and
+// six scale copies a stage was the kernel's bound.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // 4 bytes global -> shared; src_bytes == 0 writes zeros.
@@ -144,12 +159,12 @@ __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
 }
 
 // Items run expert by expert, the row tiles of a weight tile one after another.
-__device__ __forceinline__ Item decode(int64_t item, int NW, const int32_t *mts,
+__device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts,
                                        const int32_t *offs, int E) {
     Item it;
-    it.e = find_expert(mts, E, static_cast<int>(item / NW));
+    it.e = find_expert(mts, E, item / NW);
     const int ntt = mts[it.e + 1] - mts[it.e];
-    const int local = static_cast<int>(item - static_cast<int64_t>(mts[it.e]) * NW);
+    const int local = item - mts[it.e] * NW;
     it.wt = local / ntt;
     const int tt = local - it.wt * ntt;
     const int c = offs[it.e + 1] - offs[it.e];
@@ -246,10 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int NO = kSilu ? p.N / 2 : p.N;                  // outputs
     const int NW = (NO + (kSilu ? 63 : 127)) / (kSilu ? 64 : 128);
     const int nk = (p.K + BK - 1) / BK;
-    const int64_t total = static_cast<int64_t>(mts[E]) * NW;
+    const int total = mts[E] * NW;  // out fits in memory: far below 2^31
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------- TMA producer -------------------------
             int s = 0;
             uint32_t ph = 0;
@@ -257,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t issued_parity[C::STAGES];
             for (int i = 0; i < C::STAGES; ++i) issued[i] = false;
             bool ok = true;
-            for (int64_t item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
+            for (int item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
                 const Item it = decode(item, NW, mts, offs, E);
                 const int wrow = it.e * p.N + it.wt * (kSilu ? 64 : 128);
                 for (int kb = 0; kb < nk; ++kb) {
@@ -281,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ----------------------------- MMA ------------------------------
             int s = 0, tile = 0;
             uint32_t ph = 0;
             bool any = false;
-            for (int64_t item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
+            for (int item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
                 const Item it = decode(item, NW, mts, offs, E);
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
@@ -337,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
+        for (int item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
             const Item it = decode(item, NW, mts, offs, E);
             const uint8_t *src[R];
             uint32_t n[R];
@@ -383,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_first = ((warp - 4) >> 2) * 32;
         T *out = static_cast<T *>(p.out);
         int tile = 0;
-        for (int64_t item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
+        for (int item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
             const int buf = tile & 1;
             const uint32_t use = static_cast<uint32_t>(tile >> 1);
             if (!wait_bar(&ctl->tfull[buf], use & 1u, ctl, p.status)) break;
