@@ -13,18 +13,21 @@
 // A stage holds K = 256: 128 bytes of codes per row in the 128-byte swizzle,
 // loaded by TMA, and the two 4-byte words of scales of every row, which the
 // tensor core takes from TMEM in a layout of its own: a 512-byte block per 128
-// rows and 128 values of K, word r at (r % 32) * 16 + (r / 32) * 4. Two warps
-// scatter the words there from their row-major place by 4-byte cp.async (rows
-// start anywhere, so no bulk copy can), and the MMA thread copies the blocks
-// on to TMEM (tcgen05.cp) before the stage's four MMAs. Every stage has TMEM
-// columns of its own for them: a stage is refilled only after its MMAs have
-// completed, so nothing is overwritten early.
-// Roles (384 threads): a thread of warp 0 issues TMA, one of warp 1 copies
-// scales and issues MMAs, warps 2 and 3 load the scales of the weights and of the
-// rows, warps 4..11 drain the accumulators (two in TMEM, so that a tile's
-// epilogue runs under the next tile's MMAs). Items (expert, weight tile, row
-// tile) are dealt out in a fixed order; every CTA forms the plan from the
-// offsets by itself. All waits are bounded (1 s) and report a time-out in the
+// rows and 128 values of K, word r at (r % 32) * 16 + (r / 32) * 4. Rows start
+// anywhere, so no bulk copy can bring the scales there. Warps do: a lane loads four words, K = 512, of rows
+// lane, lane + 32, ... at once, and the transpose of its 4 x 4 words is its
+// 16-byte piece of four blocks (4-byte cp.async per word instead took 45 cycles
+// of the load unit per instruction, 900 a stage where the MMAs need 350). The
+// MMA thread copies the blocks on to TMEM (tcgen05.cp) before the stage's four
+// MMAs. Every stage has TMEM columns of its own for them: a stage is refilled
+// only after its MMAs have completed, so nothing is overwritten early.
+// Roles (480 threads): a thread of warp 0 issues TMA, one of warp 1 copies
+// scales and issues MMAs, warps 2..3 and 4..5 bring the scales of the weights
+// and of the rows, warps 6..13 drain the accumulators (two in TMEM, so that a
+// tile's epilogue runs under the next tile's MMAs), warp 14 works out the CTA's
+// items (expert, weight tile, row tile; dealt out in a fixed order), 32 at a
+// time, one a lane: divisions and searches that would cost every other role
+// 2000 cycles per item. All waits are bounded (1 s) and report a time-out in the
 // status word; the kernel then drains its copies and MMAs, frees TMEM and
 // returns.
 #include "mx.cuh"
@@ -38,7 +41,9 @@ constexpr int UK = 64;                // K per MMA
 constexpr int A_BYTES = WM * BK / 2;  // 16 KB
 constexpr int SF_BLOCK = 512;         // scales of 128 rows x 128 values
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kScaleWarps = 2;        // per operand
+constexpr int kThreads = 64 + 64 * kScaleWarps + 32 * kEpiWarps + 32;
+constexpr int kDeal = 32;             // items worked out at a time
 constexpr uint64_t kWaitNs = 1000000000ull;
 
 template <int NT>
@@ -48,7 +53,7 @@ struct Cfg {
     static constexpr int SFA_BYTES = 2 * SF_BLOCK;
     static constexpr int SFB_BYTES = 2 * NB * SF_BLOCK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-    static constexpr int STAGES = NT <= 32 ? 9 : 5;
+    static constexpr int STAGES = NT <= 32 ? 9 : 4;
     static constexpr int SF_COLS = 8 + 8 * NB;         // TMEM columns of a stage's scales
     static constexpr int USED_COLS = 2 * NT + STAGES * SF_COLS;
     static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
@@ -61,6 +66,8 @@ struct Ctl {
     uint64_t empty[9];
     uint64_t tfull[2];
     uint64_t tempty[2];
+    uint64_t dealt[2];   // a set of kDeal items is in place
+    uint64_t taken[2];   // every role has read the set
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -91,12 +98,6 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(p));
     return p != 0;
-}
-
-// 4 bytes global -> shared; src_bytes == 0 writes zeros.
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-                 : "memory");
 }
 
 // Box {64 two-byte columns, 16 rows, gate|up, 4 row groups} of the paired view.
@@ -144,9 +145,10 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Work item: expert e, weight tile wt, `rows` rows from t0, computed with N.
-struct Item {
-    int e, wt, t0, rows, N;
+// Work item: weight rows from wrow on (tile wt of its expert), `rows` rows from
+// t0; rows == 0 ends the list.
+struct __align__(16) Item {
+    int wrow, wt, t0, rows;
 };
 
 __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
@@ -159,21 +161,51 @@ __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
 }
 
 // Items run expert by expert, the row tiles of a weight tile one after another.
-__device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts,
-                                       const int32_t *offs, int E) {
+__device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts, const int32_t *offs,
+                                       int E, int N, int tile_outputs) {
     Item it;
-    it.e = find_expert(mts, E, item / NW);
-    const int ntt = mts[it.e + 1] - mts[it.e];
-    const int local = item - mts[it.e] * NW;
+    const int e = find_expert(mts, E, item / NW);
+    const int ntt = mts[e + 1] - mts[e];
+    const int local = item - mts[e] * NW;
     it.wt = local / ntt;
     const int tt = local - it.wt * ntt;
-    const int c = offs[it.e + 1] - offs[it.e];
+    const int c = offs[e + 1] - offs[e];
     const int ts = ((c + ntt - 1) / ntt + 15) & ~15;
-    it.t0 = offs[it.e] + tt * ts;
+    it.t0 = offs[e] + tt * ts;
     it.rows = min(ts, c - tt * ts);
-    it.N = (it.rows + 15) & ~15;
+    it.wrow = e * N + it.wt * tile_outputs;
     return it;
 }
+
+// A role's walk along the dealt items. kWarp: the whole warp walks together.
+template <bool kWarp>
+struct Walk {
+    Ctl *ctl;
+    const Item *items;  // [2][kDeal]
+    int *status;
+    int i;
+
+    __device__ __forceinline__ Walk(Ctl *c, const Item *it, int *st)
+        : ctl(c), items(it), status(st), i(0) {}
+
+    // false at the end of the list, or after a time-out
+    __device__ __forceinline__ bool next(Item &it) {
+        const int set = (i / kDeal) & 1;
+        if (i % kDeal == 0 &&
+            !wait_bar(&ctl->dealt[set], (i / (2 * kDeal)) & 1u, ctl, status))
+            return false;
+        const int4 v = *reinterpret_cast<const int4 *>(items + set * kDeal + i % kDeal);
+        it.wrow = v.x; it.wt = v.y; it.t0 = v.z; it.rows = v.w;
+        if (i % kDeal == kDeal - 1) {
+            if (kWarp) __syncwarp();
+            if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ctl->taken[set]);
+        }
+        ++i;
+        return it.rows > 0 && !aborted(ctl);
+    }
+};
+
+__device__ __forceinline__ int mma_n(const Item &it) { return (it.rows + 15) & ~15; }
 
 // silu(g) * u. For a bf16 result the fast exponential and division (2^-20
 // relative) leave its rounding alone; fp32 results take the full ones.
@@ -183,14 +215,218 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g / (1.0f + expf(-g)) * u;
 }
 
-template <typename T>
-__device__ __forceinline__ void store(T *p, float v);
-template <>
-__device__ __forceinline__ void store<float>(float *p, float v) { *p = v; }
-template <>
-__device__ __forceinline__ void store<__nv_bfloat16>(__nv_bfloat16 *p, float v) {
-    *p = __float2bfloat16_rn(v);
+// Scale warp `mine` of kScaleWarps of an operand. ROWS: WM for the weights (NO =
+// outputs of the layer), the row tile NT for the rows (NO < 0). base: the
+// operand's scale blocks in stage 0. A chunk is K = 512, two stages; the
+// operand's warps take the chunks in turn, each with two in registers, so that
+// their loads are in flight while earlier ones are stored.
+template <typename C, int ROWS, bool kPaired>
+__device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, const Item *items,
+                                             uint8_t *base, int NO, int nk, int mine) {
+    constexpr int R = (ROWS + 31) / 32;        // rows per lane
+    constexpr int NB = (ROWS + 127) / 128;     // blocks per 128 values of K
+    struct Chunk {
+        uint32_t w[4 * NB][4];                 // [row of the lane][word]
+        int stages, first;                     // its stages, counted from the kernel's first
+    };
+    const int lane = threadIdx.x & 31;
+    const bool weights = NO >= 0;
+    const uint8_t *src = weights ? p.ws : p.as;
+    const size_t pitch = static_cast<size_t>(p.K / kMxBlock);
+    const int words = p.K / kMxWord, nch = (words + 3) / 4;
+    const bool vec = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+    Walk<true> walk(ctl, items, p.status);
+    const uint8_t *row[R];
+    bool have[R];
+    int kc = nch, turn = 0, stage = 0;
+    bool more = true;
+
+    auto fetch = [&](Chunk &c) {
+        c.stages = 0;
+        for (; more; ++kc, turn = turn + 1 == kScaleWarps ? 0 : turn + 1) {
+            if (kc == nch) {
+                Item it;
+                more = walk.next(it);
+                if (!more) return;
+                kc = 0;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if (weights) {
+                        // paired: 16 gate rows and their 16 up rows in turn
+                        const int o = kPaired ? i * 16 + (lane & 15) : i * 32 + lane;
+                        have[i] = it.wt * (kPaired ? 64 : 128) + o < NO;
+                        row[i] = src + (static_cast<size_t>(it.wrow) + o + (kPaired && lane >= 16 ? NO : 0)) * pitch;
+                    } else {
+                        have[i] = i * 32 + lane < it.rows;
+                        row[i] = src + static_cast<size_t>(it.t0 + i * 32 + lane) * pitch;
+                    }
+                }
+            }
+            const int n = min(2, nk - 2 * kc);
+            if (turn == mine) {
+                c.stages = n;
+                c.first = stage;
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < R && have[i < R ? i : 0]) {
+                        const uint8_t *q = row[i < R ? i : 0] + kc * 16;
+                        if (vec) {
+                            v = __ldg(reinterpret_cast<const uint4 *>(q));
+                        } else {
+                            const uint32_t *u = reinterpret_cast<const uint32_t *>(q);
+                            const int left = words - kc * 4;
+                            v.x = __ldg(u);
+                            if (left > 1) v.y = __ldg(u + 1);
+                            if (left > 2) v.z = __ldg(u + 2);
+                            if (left > 3) v.w = __ldg(u + 3);
+                        }
+                    }
+                    c.w[i][0] = v.x; c.w[i][1] = v.y; c.w[i][2] = v.z; c.w[i][3] = v.w;
+                }
+                stage += n;
+                ++kc;
+                turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
+                return;
+            }
+            stage += n;
+        }
+    };
+    auto put = [&](const Chunk &c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h >= c.stages) break;
+            const int s = (c.first + h) % C::STAGES;
+            const uint32_t ph = static_cast<uint32_t>((c.first + h) / C::STAGES) & 1u;
+            if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) return false;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    *reinterpret_cast<uint4 *>(base + s * C::STAGE_BYTES + (j * NB + b) * SF_BLOCK + lane * 16) =
+                        make_uint4(c.w[4 * b][2 * h + j], c.w[4 * b + 1][2 * h + j],
+                                   c.w[4 * b + 2][2 * h + j], c.w[4 * b + 3][2 * h + j]);
+            fence_proxy_async_smem();  // before the tensor core's copy reads them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->full[s]);
+        }
+        return true;
+    };
+
+    Chunk c0, c1;
+    fetch(c0);
+    for (;;) {
+        fetch(c1);
+        if (c0.stages == 0 || !put(c0)) break;
+        fetch(c0);
+        if (c1.stages == 0 || !put(c1)) break;
+    }
 }
+
+// tcgen05.ld .16x256b.x4: 16 TMEM lanes x 32 columns; thread t gets lane t/4
+// (registers 4i, 4i+1) and lane t/4 + 8 (4i+2, 4i+3) of columns 8i + 2 (t % 4)
+// + {0, 1}.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// tcgen05.wait::ld that names the loads' destinations.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// Four 8 x 8 bf16 tiles in fragment layout, stored transposed: lane l names the
+// 16-byte row l % 8 of tile l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                  uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// One warp's 32 accumulator columns (rows c0.. of the tile) x its 32 TMEM lanes
+// to out. The fragments hold gate (lanes 0..15) and up (16..31) of an output in
+// the same thread and register. bf16: pairs of rows are packed, stored
+// transposed to the warp's staging rows (one per row of the tile, kPitch apart:
+// no bank conflicts) and leave as 16-byte pieces; fp32 leaves from the
+// fragments, 32 bytes of four rows at a time.
+template <bool kSilu, typename T>
+struct Drain {
+    static constexpr int kOutputs = kSilu ? 16 : 32;   // per warp
+    static constexpr int kPitch = kOutputs * 2 + 16;   // bytes
+    static constexpr int kStage = sizeof(T) == 2 ? 32 * kPitch : 0;
+
+    static __device__ __forceinline__ void run(uint32_t taddr, uint32_t stage, T *out, int f0, int NO,
+                                               int lim, int lane) {
+        uint32_t lo[16], hi[16];
+        tmem_ld_16x256b_x4(taddr, lo);
+        tmem_ld_16x256b_x4(taddr + (16u << 16), hi);
+        tmem_ld_wait(lo);
+        tmem_ld_wait(hi);
+        if constexpr (kSilu) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                lo[i] = __float_as_uint(
+                    silu_mul<sizeof(T) == 2>(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
+        }
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t at = stage + lane * kPitch;
+#pragma unroll
+            for (int h = 0; h < kOutputs / 16; ++h) {
+                const uint32_t(&v)[16] = h ? hi : lo;
+                uint32_t q[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                stmatrix_x4_trans(at + h * 32, q[0], q[2], q[4], q[6]);
+                stmatrix_x4_trans(at + h * 32 + 16, q[1], q[3], q[5], q[7]);
+            }
+            __syncwarp();
+            constexpr int kPieces = kOutputs / 8;       // 16-byte pieces of a row
+            const int col = f0 + (lane % kPieces) * 8;  // NO % 16 == 0: all 8 outputs or none
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = (i * 32 + lane) / kPieces;
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(stage + r * kPitch + (lane % kPieces) * 16)
+                             : "memory");
+                if (r < lim && col < NO)
+                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(r) * NO + col) = v;
+            }
+            __syncwarp();  // the staging rows are read before the next chunk's are written
+        } else {
+#pragma unroll
+            for (int h = 0; h < kOutputs / 16; ++h) {
+                const uint32_t(&v)[16] = h ? hi : lo;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int f = f0 + h * 16 + lane / 4 + ((i >> 1) & 1) * 8;
+                    const int r = (i >> 2) * 8 + (lane & 3) * 2 + (i & 1);
+                    if (r < lim && f < NO)
+                        out[static_cast<size_t>(r) * NO + f] = __uint_as_float(v[i]);
+                }
+            }
+        }
+    }
+};
 
 template <int NT, bool kSilu, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -200,20 +436,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::STAGES * C::STAGE_BYTES);
-    int32_t *mts = reinterpret_cast<int32_t *>(ctl + 1);  // [E+1] prefix of row tiles
+    uint8_t *stages_out = smem + C::STAGES * C::STAGE_BYTES;  // the epilogue's staging rows
+    Ctl *ctl = reinterpret_cast<Ctl *>(stages_out + kEpiWarps * Drain<kSilu, T>::kStage);
+    Item *items = reinterpret_cast<Item *>(ctl + 1);       // [2][kDeal]
+    int32_t *mts = reinterpret_cast<int32_t *>(items + 2 * kDeal);  // [E+1] prefix of row tiles
     int32_t *offs = mts + (p.E + 1);                        // [E+1]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], 1 + 64);  // the TMA thread, and every lane of two warps
+            mbar_init(&ctl->full[s], 3);  // the TMA thread and a scale warp of each operand
             mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], kEpiWarps);
+            mbar_init(&ctl->dealt[b], 1);
+            mbar_init(&ctl->taken[b], 2 + 2 * kScaleWarps + kEpiWarps);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -272,16 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t issued_parity[C::STAGES];
             for (int i = 0; i < C::STAGES; ++i) issued[i] = false;
             bool ok = true;
-            for (int item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
-                const Item it = decode(item, NW, mts, offs, E);
-                const int wrow = it.e * p.N + it.wt * (kSilu ? 64 : 128);
+            Walk<false> walk(ctl, items, p.status);
+            Item it;
+            while (ok && walk.next(it)) {
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) { ok = false; break; }
                     uint8_t *sa = smem + s * C::STAGE_BYTES;
                     mbar_arrive_expect_tx(&ctl->full[s], A_BYTES + C::B_BYTES);
                     // the maps count two-byte columns: 64 of them are K = 256
-                    if (kSilu) tma_load_4d(sa, &tmW, kb * 64, wrow / 16, &ctl->full[s]);
-                    else tma_load_2d(sa, &tmW, kb * 64, wrow, &ctl->full[s]);
+                    if (kSilu) tma_load_4d(sa, &tmW, kb * 64, it.wrow / 16, &ctl->full[s]);
+                    else tma_load_2d(sa, &tmW, kb * 64, it.wrow, &ctl->full[s]);
                     tma_load_2d(sa + A_BYTES, &tmA, kb * 64, it.t0, &ctl->full[s]);
                     issued[s] = true;
                     issued_parity[s] = ph;
@@ -301,19 +541,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             int s = 0, tile = 0;
             uint32_t ph = 0;
             bool any = false;
-            for (int item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
-                const Item it = decode(item, NW, mts, offs, E);
+            Walk<false> walk(ctl, items, p.status);
+            Item it;
+            for (; walk.next(it); ++tile) {
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
                 if (!wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * NT);
-                const uint32_t idesc[2] = {idesc_mxf4(WM, it.N, 0), idesc_mxf4(WM, it.N, 1)};
+                const int n = mma_n(it);
+                const uint32_t idesc[2] = {idesc_mxf4(WM, n, 0), idesc_mxf4(WM, n, 1)};
                 bool ok = true;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->full[s], ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    fence_proxy_async_smem();  // the scales were written by cp.async
                     const uint32_t a0 = smem_u32(smem + s * C::STAGE_BYTES);
                     const uint32_t b0 = a0 + A_BYTES, sf = b0 + C::B_BYTES;
                     const uint32_t ta = tmem_sf + static_cast<uint32_t>(s * C::SF_COLS), tb = ta + 8;
@@ -322,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scales_to_tmem(ta + 4 * j, scale_desc(sf + j * SF_BLOCK));
 #pragma unroll
                         for (int b = 0; b < C::NB; ++b)
-                            scales_to_tmem(tb + 4 * (j * C::NB + b),
+                            if (b == 0 || n > 128) scales_to_tmem(tb + 4 * (j * C::NB + b),
                                            scale_desc(sf + C::SFA_BYTES + (j * C::NB + b) * SF_BLOCK));
                     }
 #pragma unroll
@@ -343,100 +584,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(&ctl->drain, 0, globaltimer_ns() + kWaitNs);
             }
         }
-    } else if (warp < 4) {
-        // ------------- scales: warp 2 the weights', warp 3 the rows' -------------
-        const bool weights = warp == 2;
-        const size_t pitch = static_cast<size_t>(p.K / kMxBlock);
-        constexpr int RA = WM / 32, RB = NT / 32;   // rows per lane
-        constexpr int R = RA > RB ? RA : RB;
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; ok && item < total && !aborted(ctl); item += gridDim.x) {
-            const Item it = decode(item, NW, mts, offs, E);
-            const uint8_t *src[R];
-            uint32_t n[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int r = i * 32 + lane;
-                n[i] = 0u;
-                src[i] = weights ? p.ws : p.as;
-                if (weights && i < RA) {
-                    // with silu_mul, 16 gate rows and their 16 up rows in turn
-                    const int o = kSilu ? it.wt * 64 + i * 16 + (lane & 15) : it.wt * 128 + r;
-                    if (o < NO) {
-                        n[i] = 4u;
-                        src[i] += (static_cast<size_t>(it.e) * p.N + o + (kSilu && lane >= 16 ? NO : 0)) * pitch;
-                    }
-                } else if (!weights && i < RB && r < it.rows) {
-                    n[i] = 4u;
-                    src[i] += static_cast<size_t>(it.t0 + r) * pitch;
-                }
-            }
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) { ok = false; break; }
-                const uint32_t sf = smem_u32(smem + s * C::STAGE_BYTES) + A_BYTES + C::B_BYTES +
-                                    (weights ? 0 : C::SFA_BYTES) + lane * 16;
-                const bool two = kb * BK + kMxWord < p.K;  // K may end inside the stage
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    if (i < (weights ? RA : RB)) {
-                        const uint32_t dst = sf + (i >> 2) * SF_BLOCK + (i & 3) * 4;
-                        const uint32_t next = (weights ? 1 : C::NB) * SF_BLOCK;
-                        cp_async_4(dst, src[i] + kb * 8, n[i]);
-                        cp_async_4(dst + next, src[i] + kb * 8 + (two ? 4 : 0), two ? n[i] : 0u);
-                    }
-                }
-                cp_async_arrive_noinc(&ctl->full[s]);
-                if (++s == C::STAGES) { s = 0; ph ^= 1u; }
-            }
+    } else if (warp < 2 + kScaleWarps) {
+        bring_scales<C, WM, kSilu>(p, ctl, items, smem + A_BYTES + C::B_BYTES, NO, nk, warp - 2);
+    } else if (warp < 2 + 2 * kScaleWarps) {
+        bring_scales<C, NT, false>(p, ctl, items, smem + A_BYTES + C::B_BYTES + C::SFA_BYTES, -1, nk,
+                                   warp - 2 - kScaleWarps);
+    } else if (warp == kThreads / 32 - 1) {
+        // ------------------------- item dealer --------------------------
+        for (int c = 0;; ++c) {
+            if (c >= 2 && !wait_bar(&ctl->taken[c & 1], ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
+            const int64_t item = blockIdx.x + (static_cast<int64_t>(c) * kDeal + lane) * gridDim.x;
+            Item it = {0, 0, 0, 0};
+            if (item < total)
+                it = decode(static_cast<int>(item), NW, mts, offs, E, p.N, kSilu ? 64 : 128);
+            items[(c & 1) * kDeal + lane] = it;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->dealt[c & 1]);
+            if (__any_sync(0xffffffffu, it.rows == 0) || aborted(ctl)) break;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // --------------------------- epilogue ---------------------------
         const int q = warp & 3;                   // TMEM lane quarter of this warp
-        const int c_first = ((warp - 4) >> 2) * 32;
+        const int ew = warp - 2 - 2 * kScaleWarps;
+        const int c_first = (ew >> 2) * 32;       // its 32-column chunks, every second
+        const uint32_t stage = smem_u32(stages_out) + ew * Drain<kSilu, T>::kStage;
         T *out = static_cast<T *>(p.out);
         int tile = 0;
-        for (int item = blockIdx.x; item < total && !aborted(ctl); item += gridDim.x, ++tile) {
+        Walk<true> walk(ctl, items, p.status);
+        Item it;
+        for (; walk.next(it); ++tile) {
             const int buf = tile & 1;
             const uint32_t use = static_cast<uint32_t>(tile >> 1);
             if (!wait_bar(&ctl->tfull[buf], use & 1u, ctl, p.status)) break;
             tc_fence_after();
-            const Item it = decode(item, NW, mts, offs, E);
             const uint32_t t_lane = tmem_base + static_cast<uint32_t>(buf * NT) +
                                     (static_cast<uint32_t>(q * 32) << 16);
-            // lanes 0..15: gate of outputs f, lanes 16..31: up of the same f
-            const int f = kSilu ? it.wt * 64 + q * 16 + (lane & 15) : it.wt * 128 + q * 32 + lane;
+            const int f0 = kSilu ? it.wt * 64 + q * 16 : it.wt * 128 + q * 32;
 #pragma unroll 1
-            for (int c0 = c_first; c0 < it.rows; c0 += 32 * (kEpiWarps / 4)) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(t_lane + c0, v);
-                tmem_ld_wait(v);
-                if constexpr (kSilu) {
-                    // the gate lane finishes rows 0..15 of the chunk, the up lane 16..31
-                    const bool is_gate = lane < 16;
-                    const int rb = c0 + (is_gate ? 0 : 16);
-                    const int lim = f < NO ? it.rows - rb : 0;
-                    T *dst = out + static_cast<size_t>(it.t0 + rb) * NO + f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float lo = __uint_as_float(v[j]), hi = __uint_as_float(v[16 + j]);
-                        const float got = __shfl_xor_sync(0xffffffffu, is_gate ? hi : lo, 16);
-                        const float r = silu_mul<sizeof(T) == 2>(is_gate ? lo : got, is_gate ? got : hi);
-                        if (j < lim) store<T>(dst, r);
-                        dst += NO;
-                    }
-                } else {
-                    const int lim = f < NO ? it.rows - c0 : 0;
-                    T *dst = out + static_cast<size_t>(it.t0 + c0) * NO + f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j < lim) store<T>(dst, __uint_as_float(v[j]));
-                        dst += NO;
-                    }
-                }
-            }
+            for (int c0 = c_first; c0 < it.rows; c0 += 32 * (kEpiWarps / 4))
+                Drain<kSilu, T>::run(t_lane + c0, stage, out + static_cast<size_t>(it.t0 + c0) * NO, f0,
+                                     NO, it.rows - c0, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
@@ -466,7 +653,8 @@ int launch(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
     if (rc != MOE_OK) return rc;
     if ((rc = tc_encode_2d(&a, p.a, p.rows, p.K / 4, NT)) != MOE_OK) return rc;
     auto kern = mx_matmul_kernel<NT, kSilu, T>;
-    const size_t smem = 1024 + C::STAGES * C::STAGE_BYTES + sizeof(Ctl) + 2 * (p.E + 1) * sizeof(int32_t);
+    const size_t smem = 1024 + C::STAGES * C::STAGE_BYTES + kEpiWarps * Drain<kSilu, T>::kStage +
+                        sizeof(Ctl) + 2 * kDeal * sizeof(Item) + 2 * (p.E + 1) * sizeof(int32_t);
     if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
     // no more CTAs than there can be items
     const int64_t tiles = static_cast<int64_t>(p.rows / NT + p.E) *
