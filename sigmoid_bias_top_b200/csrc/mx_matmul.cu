@@ -30,45 +30,56 @@
 // 2000 cycles per item. All waits are bounded (1 s) and report a time-out in the
 // status word; the kernel then drains its copies and MMAs, frees TMEM and
 // returns.
+#include <cooperative_groups.h>
+
 #include "mx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace moe {
 namespace {
 
-constexpr int WM = 128;               // weight rows per tile
+constexpr int WM = 128;               // weight rows per CTA and tile
 constexpr int BK = 256;               // K per stage (128 bytes of codes per row)
 constexpr int UK = 64;                // K per MMA
 constexpr int A_BYTES = WM * BK / 2;  // 16 KB
 constexpr int SF_BLOCK = 512;         // scales of 128 rows x 128 values
 constexpr int kEpiWarps = 8;
 constexpr int kScaleWarps = 2;        // per operand
-constexpr int kThreads = 64 + 64 * kScaleWarps + 32 * kEpiWarps + 32;
+constexpr int kThreads = 64 + 64 * kScaleWarps + 32 * kEpiWarps + 64;
 constexpr int kDeal = 32;             // items worked out at a time
+constexpr int kMaxStages = 9;
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;  // shared::cluster address in the pair's even CTA
 
-template <int NT>
+// NT: rows of a tile at most. kPair: a tile is shared by two CTAs.
+template <int NT, bool kPair>
 struct Cfg {
     static constexpr int NB = (NT + 127) / 128;        // 128-row scale blocks of the rows
-    static constexpr int B_BYTES = NT * BK / 2;
+    static constexpr int B_ROWS = kPair ? NT / 2 : NT;
+    static constexpr int B_BYTES = B_ROWS * BK / 2;
     static constexpr int SFA_BYTES = 2 * SF_BLOCK;
     static constexpr int SFB_BYTES = 2 * NB * SF_BLOCK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-    static constexpr int STAGES = NT <= 32 ? 9 : 4;
+    static constexpr int STAGES = NT <= 32 ? 9 : 5;
     static constexpr int SF_COLS = 8 + 8 * NB;         // TMEM columns of a stage's scales
     static constexpr int USED_COLS = 2 * NT + STAGES * SF_COLS;
     static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
-    static_assert(USED_COLS <= 512, "TMEM");
+    static constexpr int N_STEP = kPair ? 32 : 16;     // the MMA's N is a multiple of it
+    static_assert(USED_COLS <= 512 && STAGES <= kMaxStages, "TMEM");
     static_assert(B_BYTES % 1024 == 0 && (SFA_BYTES + SFB_BYTES) % 1024 == 0, "swizzle atoms");
 };
 
-struct Ctl {
-    uint64_t full[9];
-    uint64_t empty[9];
+struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
+    uint64_t full[kMaxStages];    // codes and scales are in place
+    uint64_t scaled[kMaxStages];  // pairs: this CTA's scales are in shared memory
+    uint64_t peer[kMaxStages];    // leader: the other CTA's are
+    uint64_t empty[kMaxStages];   // the stage's MMAs are done
     uint64_t tfull[2];
     uint64_t tempty[2];
-    uint64_t dealt[2];   // a set of kDeal items is in place
-    uint64_t taken[2];   // every role has read the set
-    uint64_t drain;
+    uint64_t dealt[2];            // a set of kDeal items is in place
+    uint64_t taken[2];            // every role has read the set
+    uint64_t drain, copied;
     uint32_t tmem_base;
     int abort;
 };
@@ -100,27 +111,151 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Box {64 two-byte columns, 16 rows, gate|up, 4 row groups} of the paired view.
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int x, int group,
-                                            uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group), "r"(smem_u32(bar))
-        : "memory");
+// Arrival on the barrier at the same offset in the pair's leader. What it has to
+// order is local to this SM and done by then: TMEM reads that the caller fenced,
+// or scales in this CTA's shared memory, which their writers fenced towards the
+// async proxy and this thread has seen (an mbarrier wait in this CTA). No global
+// access has to be ordered, so there is no release to the cluster, which waits
+// for all of the SM's accesses in flight: 1300 cycles a stage.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
+
+// wait_bar on a barrier that threads of the other CTA arrive on.
+__device__ __forceinline__ bool wait_bar_cluster(uint64_t *bar, uint32_t parity, Ctl *ctl, int *status) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t deadline = 0;
+    for (uint32_t i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0u) {
+            const uint64_t now = globaltimer_ns();
+            if (deadline == 0) deadline = now + kWaitNs;
+            else if (now > deadline) break;
+        }
+    }
+    set_status(status, kStatusTimeout);
+    atomicExch(&ctl->abort, 1);
+    return false;
+}
+
+// The instructions of one CTA, or of a pair (cta_group::2: issued by the
+// leader; loads of both CTAs complete on the leader's barrier, commits arrive
+// in both).
+template <bool kPair>
+struct Tc {
+    static __device__ __forceinline__ void alloc(uint32_t *dst, uint32_t cols) {
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(dst)),
+                         "r"(cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(dst, cols);
+            tmem_relinquish();
+        }
+    }
+    static __device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t cols) {
+        if constexpr (kPair)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                         : "memory");
+        else
+            tmem_dealloc(taddr, cols);
+    }
+    static __device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *m, int x, int y,
+                                                   uint64_t *bar) {
+        if constexpr (kPair)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar) & kPeerBitMask)
+                : "memory");
+        else
+            tma_load_2d(dst, m, x, y, bar);
+    }
+    // Box {64 two-byte columns, 16 rows, gate|up, 4 row groups} of the paired-row view.
+    static __device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *m, int x, int group,
+                                                   uint64_t *bar) {
+        if constexpr (kPair)
+            asm volatile(
+                "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group),
+                "r"(smem_u32(bar) & kPeerBitMask)
+                : "memory");
+        else
+            asm volatile(
+                "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group),
+                "r"(smem_u32(bar))
+                : "memory");
+    }
+    // 32 rows x 16 bytes of shared memory (each CTA's own) to 4 TMEM columns,
+    // repeated in the four 32-lane quarters.
+    static __device__ __forceinline__ void scales(uint32_t taddr, uint64_t desc) {
+        if constexpr (kPair)
+            asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        else
+            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    }
+    static __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                               uint32_t accumulate) {
+        if constexpr (kPair)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %6, 0;\n\t"
+                "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                    "r"(d_tmem),
+                "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %6, 0;\n\t"
+                "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                    "r"(d_tmem),
+                "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+                : "memory");
+    }
+    // one arrival on `bar`, in both CTAs of a pair, when this thread's tcgen05 work is done
+    static __device__ __forceinline__ void commit(uint64_t *bar) {
+        if constexpr (kPair)
+            asm volatile(
+                "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                " [%0], m;\n\t}" ::"r"(smem_u32(bar))
+                : "memory");
+        else
+            umma_commit(bar);
+    }
+    // the same on this CTA's barrier alone
+    static __device__ __forceinline__ void commit_here(uint64_t *bar) {
+        if constexpr (kPair)
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                             smem_u32(bar))
+                         : "memory");
+        else
+            umma_commit(bar);
+    }
+};
 
 // Descriptor of a 512-byte scale block: no swizzle, 8-row groups of 16-byte
 // rows 128 bytes apart, descriptor version 1.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 |
            static_cast<uint64_t>(1) << 46;
-}
-
-// 32 rows x 16 bytes of shared memory to 4 TMEM columns, repeated in the four
-// 32-lane quarters.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales,
@@ -131,18 +266,6 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int h) {
            | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23)  // N / 8; E8M0
            | (static_cast<uint32_t>(M >> 4) << 24)
            | (static_cast<uint32_t>(2 * h) << 29);       // A scale byte
-}
-
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-            "r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
 }
 
 // Work item: weight rows from wrow on (tile wt of its expert), `rows` rows from
@@ -162,7 +285,7 @@ __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
 
 // Items run expert by expert, the row tiles of a weight tile one after another.
 __device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts, const int32_t *offs,
-                                       int E, int N, int tile_outputs) {
+                                       int E, int N, int tile_outputs, int n_step) {
     Item it;
     const int e = find_expert(mts, E, item / NW);
     const int ntt = mts[e + 1] - mts[e];
@@ -170,7 +293,7 @@ __device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts, con
     it.wt = local / ntt;
     const int tt = local - it.wt * ntt;
     const int c = offs[e + 1] - offs[e];
-    const int ts = ((c + ntt - 1) / ntt + 15) & ~15;
+    const int ts = ((c + ntt - 1) / ntt + n_step - 1) / n_step * n_step;
     it.t0 = offs[e] + tt * ts;
     it.rows = min(ts, c - tt * ts);
     it.wrow = e * N + it.wt * tile_outputs;
@@ -205,8 +328,6 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ int mma_n(const Item &it) { return (it.rows + 15) & ~15; }
-
 // silu(g) * u. For a bf16 result the fast exponential and division (2^-20
 // relative) leave its rounding alone; fp32 results take the full ones.
 template <bool kFast>
@@ -216,17 +337,20 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // Scale warp `mine` of kScaleWarps of an operand. ROWS: WM for the weights (NO =
-// outputs of the layer), the row tile NT for the rows (NO < 0). base: the
-// operand's scale blocks in stage 0. A chunk is K = 512, two stages; the
-// operand's warps take the chunks in turn, each with two in registers, so that
-// their loads are in flight while earlier ones are stored.
-template <typename C, int ROWS, bool kPaired>
+// outputs of the layer, o_base = first of the CTA's outputs in the tile), the
+// row tile NT for the rows (NO < 0). base: the operand's scale blocks in stage
+// 0. A chunk is K = 512, two stages; the operand's warps take the chunks in
+// turn, each with two in registers, so that their loads are in flight while
+// earlier ones are stored. Rows past the tile's end take the last one's scales:
+// their products are never stored. kVec: rows of scales are whole 16-byte words.
+template <typename C, int ROWS, bool kPaired, bool kPair, bool kVec>
 __device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, const Item *items,
-                                             uint8_t *base, int NO, int nk, int mine) {
+                                             uint8_t *base, int NO, int o_base, int tile_outputs,
+                                             int nk, int mine) {
     constexpr int R = (ROWS + 31) / 32;        // rows per lane
     constexpr int NB = (ROWS + 127) / 128;     // blocks per 128 values of K
     struct Chunk {
-        uint32_t w[4 * NB][4];                 // [row of the lane][word]
+        uint4 w[R];                            // four words of each of the lane's rows
         int stages, first;                     // its stages, counted from the kernel's first
     };
     const int lane = threadIdx.x & 31;
@@ -234,10 +358,8 @@ __device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, 
     const uint8_t *src = weights ? p.ws : p.as;
     const size_t pitch = static_cast<size_t>(p.K / kMxBlock);
     const int words = p.K / kMxWord, nch = (words + 3) / 4;
-    const bool vec = p.K % 512 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
     Walk<true> walk(ctl, items, p.status);
     const uint8_t *row[R];
-    bool have[R];
     int kc = nch, turn = 0, stage = 0;
     bool more = true;
 
@@ -249,17 +371,14 @@ __device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, 
                 more = walk.next(it);
                 if (!more) return;
                 kc = 0;
+                const uint8_t *first = src + static_cast<size_t>(weights ? it.wrow : it.t0) * pitch;
+                const int last = weights ? NO - 1 - it.wt * tile_outputs : it.rows - 1;
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    if (weights) {
-                        // paired: 16 gate rows and their 16 up rows in turn
-                        const int o = kPaired ? i * 16 + (lane & 15) : i * 32 + lane;
-                        have[i] = it.wt * (kPaired ? 64 : 128) + o < NO;
-                        row[i] = src + (static_cast<size_t>(it.wrow) + o + (kPaired && lane >= 16 ? NO : 0)) * pitch;
-                    } else {
-                        have[i] = i * 32 + lane < it.rows;
-                        row[i] = src + static_cast<size_t>(it.t0 + i * 32 + lane) * pitch;
-                    }
+                    // paired: 16 gate rows and their 16 up rows in turn
+                    int o = weights ? o_base + (kPaired ? i * 16 + (lane & 15) : i * 32 + lane) : i * 32 + lane;
+                    o = min(o, last) + (kPaired && lane >= 16 ? NO : 0);
+                    row[i] = first + static_cast<size_t>(o) * pitch;
                 }
             }
             const int n = min(2, nk - 2 * kc);
@@ -267,22 +386,17 @@ __device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, 
                 c.stages = n;
                 c.first = stage;
 #pragma unroll
-                for (int i = 0; i < 4 * NB; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (i < R && have[i < R ? i : 0]) {
-                        const uint8_t *q = row[i < R ? i : 0] + kc * 16;
-                        if (vec) {
-                            v = __ldg(reinterpret_cast<const uint4 *>(q));
-                        } else {
-                            const uint32_t *u = reinterpret_cast<const uint32_t *>(q);
-                            const int left = words - kc * 4;
-                            v.x = __ldg(u);
-                            if (left > 1) v.y = __ldg(u + 1);
-                            if (left > 2) v.z = __ldg(u + 2);
-                            if (left > 3) v.w = __ldg(u + 3);
-                        }
+                for (int i = 0; i < R; ++i) {
+                    if constexpr (kVec) {
+                        c.w[i] = __ldg(reinterpret_cast<const uint4 *>(row[i] + kc * 16));
+                    } else {
+                        const uint32_t *u = reinterpret_cast<const uint32_t *>(row[i] + kc * 16);
+                        const int left = words - kc * 4;
+                        c.w[i].x = __ldg(u);
+                        c.w[i].y = left > 1 ? __ldg(u + 1) : 0u;
+                        c.w[i].z = left > 2 ? __ldg(u + 2) : 0u;
+                        c.w[i].w = left > 3 ? __ldg(u + 3) : 0u;
                     }
-                    c.w[i][0] = v.x; c.w[i][1] = v.y; c.w[i][2] = v.z; c.w[i][3] = v.w;
                 }
                 stage += n;
                 ++kc;
@@ -302,13 +416,19 @@ __device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, 
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b) {
+                    uint32_t v[4];  // word 2h + j of the lane's four rows of the block
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 &w = c.w[4 * b + i < R ? 4 * b + i : R - 1];
+                        v[i] = h == 0 ? (j == 0 ? w.x : w.y) : (j == 0 ? w.z : w.w);
+                    }
                     *reinterpret_cast<uint4 *>(base + s * C::STAGE_BYTES + (j * NB + b) * SF_BLOCK + lane * 16) =
-                        make_uint4(c.w[4 * b][2 * h + j], c.w[4 * b + 1][2 * h + j],
-                                   c.w[4 * b + 2][2 * h + j], c.w[4 * b + 3][2 * h + j]);
+                        make_uint4(v[0], v[1], v[2], v[3]);
+                }
             fence_proxy_async_smem();  // before the tensor core's copy reads them
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->full[s]);
+            if (lane == 0) mbar_arrive(kPair ? &ctl->scaled[s] : &ctl->full[s]);
         }
         return true;
     };
@@ -428,11 +548,32 @@ struct Drain {
     }
 };
 
-template <int NT, bool kSilu, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
-    mx_matmul_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                     MxMatmulParams p) {
-    using C = Cfg<NT>;
+template <typename C>
+__device__ __forceinline__ int mma_n(const Item &it) {
+    return (it.rows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
+}
+
+// A stage's scale blocks (shared address sf) to its TMEM columns; two: the rows
+// fill more than one block.
+template <typename C, bool kPair>
+__device__ __forceinline__ void copy_scales(uint32_t sf, uint32_t taddr, bool two) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        Tc<kPair>::scales(taddr + 4 * j, scale_desc(sf + j * SF_BLOCK));
+#pragma unroll
+        for (int b = 0; b < C::NB; ++b)
+            if (b == 0 || two)
+                Tc<kPair>::scales(taddr + 8 + 4 * (j * C::NB + b),
+                                  scale_desc(sf + C::SFA_BYTES + (j * C::NB + b) * SF_BLOCK));
+    }
+}
+
+template <int NT, bool kPair, bool kSilu, typename T>
+__device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUtensorMap &tmA,
+                                               const MxMatmulParams &p) {
+    using C = Cfg<NT, kPair>;
+    using X = Tc<kPair>;
+    constexpr int kCtas = kPair ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -443,26 +584,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t *offs = mts + (p.E + 1);                        // [E+1]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
+    const int half = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // rank in the cluster of two
+    const bool leader = half == 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&ctl->full[s], 3);  // the TMA thread and a scale warp of each operand
+            // the TMA thread, and a scale warp of each operand or, for pairs, the
+            // commit of the scales' copies
+            mbar_init(&ctl->full[s], kPair ? 2 : 3);
+            mbar_init(&ctl->scaled[s], 2);  // a scale warp of each operand
+            mbar_init(&ctl->peer[s], 1);
             mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
-            mbar_init(&ctl->tempty[b], kEpiWarps);
+            mbar_init(&ctl->tempty[b], kCtas * kEpiWarps);
             mbar_init(&ctl->dealt[b], 1);
-            mbar_init(&ctl->taken[b], 2 + 2 * kScaleWarps + kEpiWarps);
+            // TMA, scale and epilogue warps; MMA thread of the leader, copy threads of pairs
+            mbar_init(&ctl->taken[b], 1 + 2 * kScaleWarps + kEpiWarps + (kPair ? leader ? 2 : 1 : 1));
         }
         mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->copied, 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
-        tmem_alloc(&ctl->tmem_base, C::TMEM_COLS);
-        tmem_relinquish();
-    }
+    if (warp == 1) X::alloc(&ctl->tmem_base, C::TMEM_COLS);
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmA);
@@ -493,13 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair) cg::this_cluster().sync();  // barriers and TMEM of both CTAs are ready
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
     const uint32_t tmem_sf = tmem_base + 2 * NT;
 
     const int NO = kSilu ? p.N / 2 : p.N;                  // outputs
-    const int NW = (NO + (kSilu ? 63 : 127)) / (kSilu ? 64 : 128);
+    constexpr int kCtaOutputs = kSilu ? 64 : 128;
+    constexpr int kOutputs = kCtaOutputs * kCtas;          // outputs of a tile
+    const int NW = (NO + kOutputs - 1) / kOutputs;
     const int nk = (p.K + BK - 1) / BK;
     const int total = mts[E] * NW;  // out fits in memory: far below 2^31
 
@@ -515,28 +664,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             Walk<false> walk(ctl, items, p.status);
             Item it;
             while (ok && walk.next(it)) {
+                const int wrow = it.wrow + half * kCtaOutputs;
+                const int trow = it.t0 + half * (mma_n<C>(it) / 2);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) { ok = false; break; }
                     uint8_t *sa = smem + s * C::STAGE_BYTES;
-                    mbar_arrive_expect_tx(&ctl->full[s], A_BYTES + C::B_BYTES);
+                    if (leader) mbar_arrive_expect_tx(&ctl->full[s], kCtas * (A_BYTES + C::B_BYTES));
                     // the maps count two-byte columns: 64 of them are K = 256
-                    if (kSilu) tma_load_4d(sa, &tmW, kb * 64, it.wrow / 16, &ctl->full[s]);
-                    else tma_load_2d(sa, &tmW, kb * 64, it.wrow, &ctl->full[s]);
-                    tma_load_2d(sa + A_BYTES, &tmA, kb * 64, it.t0, &ctl->full[s]);
+                    if (kSilu) X::load_4d(sa, &tmW, kb * 64, wrow / 16, &ctl->full[s]);
+                    else X::load_2d(sa, &tmW, kb * 64, wrow, &ctl->full[s]);
+                    X::load_2d(sa + A_BYTES, &tmA, kb * 64, trow, &ctl->full[s]);
                     issued[s] = true;
                     issued_parity[s] = ph;
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
                 }
             }
+            // (a pair's copies complete on the leader's barriers)
             if (!ok || aborted(ctl)) {  // let the other roles leave and our own copies land
                 atomicExch(&ctl->abort, 1);
                 const uint64_t dl = globaltimer_ns() + kWaitNs;
-                for (int i = 0; i < C::STAGES; ++i)
+                for (int i = 0; leader && i < C::STAGES; ++i)
                     if (issued[i]) mbar_wait(&ctl->full[i], issued_parity[i], dl);
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (leader && elect_one()) {
             // ----------------------------- MMA ------------------------------
             int s = 0, tile = 0;
             uint32_t ph = 0;
@@ -546,57 +698,93 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; walk.next(it); ++tile) {
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
-                if (!wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)) break;
+                if (kPair ? !wait_bar_cluster(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)
+                          : !wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status))
+                    break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * NT);
-                const int n = mma_n(it);
-                const uint32_t idesc[2] = {idesc_mxf4(WM, n, 0), idesc_mxf4(WM, n, 1)};
+                const int n = mma_n<C>(it);
+                const uint32_t idesc[2] = {idesc_mxf4(kCtas * WM, n, 0), idesc_mxf4(kCtas * WM, n, 1)};
                 bool ok = true;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->full[s], ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a0 = smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t b0 = a0 + A_BYTES, sf = b0 + C::B_BYTES;
+                    const uint32_t b0 = a0 + A_BYTES;
                     const uint32_t ta = tmem_sf + static_cast<uint32_t>(s * C::SF_COLS), tb = ta + 8;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        scales_to_tmem(ta + 4 * j, scale_desc(sf + j * SF_BLOCK));
-#pragma unroll
-                        for (int b = 0; b < C::NB; ++b)
-                            if (b == 0 || n > 128) scales_to_tmem(tb + 4 * (j * C::NB + b),
-                                           scale_desc(sf + C::SFA_BYTES + (j * C::NB + b) * SF_BLOCK));
-                    }
+                    if constexpr (!kPair) copy_scales<C, kPair>(b0 + C::B_BYTES, ta, n > 128);
 #pragma unroll
                     for (int kk = 0; kk < BK / UK; ++kk)
-                        umma_mxf4(d_tmem, sw128_kmajor_desc(a0 + kk * UK / 2),
-                                  sw128_kmajor_desc(b0 + kk * UK / 2), idesc[kk & 1],
-                                  ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1),
-                                  (kb | kk) != 0 ? 1u : 0u);
+                        X::mma(d_tmem, sw128_kmajor_desc(a0 + kk * UK / 2),
+                               sw128_kmajor_desc(b0 + kk * UK / 2), idesc[kk & 1],
+                               ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1),
+                               (kb | kk) != 0 ? 1u : 0u);
                     any = true;
-                    umma_commit(&ctl->empty[s]);
+                    X::commit(&ctl->empty[s]);
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
-                umma_commit(&ctl->tfull[buf]);
+                X::commit(&ctl->tfull[buf]);
             }
             if (any) {
-                umma_commit(&ctl->drain);
+                X::commit_here(&ctl->drain);
                 mbar_wait(&ctl->drain, 0, globaltimer_ns() + kWaitNs);
             }
         }
-    } else if (warp < 2 + kScaleWarps) {
-        bring_scales<C, WM, kSilu>(p, ctl, items, smem + A_BYTES + C::B_BYTES, NO, nk, warp - 2);
     } else if (warp < 2 + 2 * kScaleWarps) {
-        bring_scales<C, NT, false>(p, ctl, items, smem + A_BYTES + C::B_BYTES + C::SFA_BYTES, -1, nk,
-                                   warp - 2 - kScaleWarps);
+        // ---------------------------- scales ----------------------------
+        const bool weights = warp < 2 + kScaleWarps;
+        const int mine = (warp - 2) % kScaleWarps;
+        uint8_t *sf = smem + A_BYTES + C::B_BYTES;
+        const bool vec = p.K % 512 == 0 &&
+                         (reinterpret_cast<uintptr_t>(weights ? p.ws : p.as) & 15u) == 0;
+        if (weights && vec)
+            bring_scales<C, WM, kSilu, kPair, true>(p, ctl, items, sf, NO, half * kCtaOutputs, kOutputs, nk, mine);
+        else if (weights)
+            bring_scales<C, WM, kSilu, kPair, false>(p, ctl, items, sf, NO, half * kCtaOutputs, kOutputs, nk, mine);
+        else if (vec)
+            bring_scales<C, NT, false, kPair, true>(p, ctl, items, sf + C::SFA_BYTES, -1, 0, 0, nk, mine);
+        else
+            bring_scales<C, NT, false, kPair, false>(p, ctl, items, sf + C::SFA_BYTES, -1, 0, 0, nk, mine);
     } else if (warp == kThreads / 32 - 1) {
+        if (kPair && elect_one()) {
+            // ---- pairs: scales on to TMEM by the leader, told by the other CTA ----
+            int s = 0;
+            uint32_t ph = 0;
+            bool any = false, ok = true;
+            Walk<false> walk(ctl, items, p.status);
+            Item it;
+            while (ok && walk.next(it)) {
+                const bool two = mma_n<C>(it) > 128;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!wait_bar(&ctl->scaled[s], ph, ctl, p.status)) { ok = false; break; }
+                    if (leader) {
+                        if (!wait_bar_cluster(&ctl->peer[s], ph, ctl, p.status)) { ok = false; break; }
+                        tc_fence_after();
+                        copy_scales<C, kPair>(smem_u32(smem + s * C::STAGE_BYTES) + A_BYTES + C::B_BYTES,
+                                              tmem_sf + static_cast<uint32_t>(s * C::SF_COLS), two);
+                        X::commit_here(&ctl->full[s]);
+                        any = true;
+                    } else {
+                        mbar_arrive_leader(&ctl->peer[s]);
+                    }
+                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                }
+            }
+            if (any) {  // no copy is in flight when the kernel ends
+                X::commit_here(&ctl->copied);
+                mbar_wait(&ctl->copied, 0, globaltimer_ns() + kWaitNs);
+            }
+        }
+    } else if (warp == kThreads / 32 - 2) {
         // ------------------------- item dealer --------------------------
         for (int c = 0;; ++c) {
             if (c >= 2 && !wait_bar(&ctl->taken[c & 1], ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
-            const int64_t item = blockIdx.x + (static_cast<int64_t>(c) * kDeal + lane) * gridDim.x;
+            const int64_t item = blockIdx.x / kCtas +
+                                 (static_cast<int64_t>(c) * kDeal + lane) * (gridDim.x / kCtas);
             Item it = {0, 0, 0, 0};
             if (item < total)
-                it = decode(static_cast<int>(item), NW, mts, offs, E, p.N, kSilu ? 64 : 128);
+                it = decode(static_cast<int>(item), NW, mts, offs, E, p.N, kOutputs, C::N_STEP);
             items[(c & 1) * kDeal + lane] = it;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->dealt[c & 1]);
@@ -619,56 +807,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t t_lane = tmem_base + static_cast<uint32_t>(buf * NT) +
                                     (static_cast<uint32_t>(q * 32) << 16);
-            const int f0 = kSilu ? it.wt * 64 + q * 16 : it.wt * 128 + q * 32;
+            const int f0 = it.wt * kOutputs + half * kCtaOutputs + q * (kSilu ? 16 : 32);
 #pragma unroll 1
             for (int c0 = c_first; c0 < it.rows; c0 += 32 * (kEpiWarps / 4))
                 Drain<kSilu, T>::run(t_lane + c0, stage, out + static_cast<size_t>(it.t0 + c0) * NO, f0,
                                      NO, it.rows - c0, lane);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->tempty[buf]);
+            if (lane == 0) {
+                if constexpr (kPair) mbar_arrive_leader(&ctl->tempty[buf]);
+                else mbar_arrive(&ctl->tempty[buf]);
+            }
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cg::this_cluster().sync();  // the leader's work in both CTAs has drained
     tc_fence_after();
     if (warp == 1) {
         __syncwarp();
-        tmem_dealloc(tmem_base, C::TMEM_COLS);
+        X::dealloc(tmem_base, C::TMEM_COLS);
     }
+}
+
+template <int NT, bool kSilu, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_matmul_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                     MxMatmulParams p) {
+    mx_matmul_body<NT, false, kSilu, T>(tmW, tmA, p);
+}
+
+template <int NT, bool kSilu, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mx_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmW,
+                          const __grid_constant__ CUtensorMap tmA, MxMatmulParams p) {
+    mx_matmul_body<NT, true, kSilu, T>(tmW, tmA, p);
 }
 
 // Device-side failures of calls without a context (moe_mx_status).
 __device__ int g_mx_status;
 
-template <int NT, bool kSilu, typename T>
+// CTA pairs that can be resident at once (an SM without a partner in its GPC
+// cannot host half a pair), at most one pair per two SMs.
+int resident_pairs(const void *kern, size_t smem, int n_sm) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_sm / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        n = n_sm / 2;
+    }
+    return n < n_sm / 2 ? n : n_sm / 2;
+}
+
+template <int NT, bool kPair, bool kSilu, typename T>
 int launch(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
-    using C = Cfg<NT>;
+    using C = Cfg<NT, kPair>;
     CUtensorMap w, a;
     int rc;
     const uint64_t wrows = static_cast<uint64_t>(p.E) * p.N;
     if (kSilu) rc = tc_encode_pair_4d(&w, p.w, wrows, p.K / 4, p.N / 2);
     else rc = tc_encode_2d(&w, p.w, wrows, p.K / 4, WM);
     if (rc != MOE_OK) return rc;
-    if ((rc = tc_encode_2d(&a, p.a, p.rows, p.K / 4, NT)) != MOE_OK) return rc;
-    auto kern = mx_matmul_kernel<NT, kSilu, T>;
+    if ((rc = tc_encode_2d(&a, p.a, p.rows, p.K / 4, C::B_ROWS)) != MOE_OK) return rc;
     const size_t smem = 1024 + C::STAGES * C::STAGE_BYTES + kEpiWarps * Drain<kSilu, T>::kStage +
                         sizeof(Ctl) + 2 * kDeal * sizeof(Item) + 2 * (p.E + 1) * sizeof(int32_t);
-    if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
     // no more CTAs than there can be items
-    const int64_t tiles = static_cast<int64_t>(p.rows / NT + p.E) *
-                          ((p.N + (WM - 1)) / WM);
-    const int grid = static_cast<int>(tiles < n_sm ? tiles : n_sm);
-    return launch_k(kern, dim3(grid), dim3(kThreads), smem, s, w, a, p);
+    const int64_t items = static_cast<int64_t>(p.rows / NT + p.E) *
+                          ((p.N + (kPair ? 2 : 1) * WM - 1) / ((kPair ? 2 : 1) * WM));
+    if constexpr (kPair) {
+        auto kern = mx_matmul_pair_kernel<NT, kSilu, T>;
+        if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
+        static int resident = 0;  // per kernel, for the device model of the process
+        if (resident == 0) resident = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
+        const int pairs = static_cast<int>(items < resident ? items : resident);
+        return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, w, a, p);
+    } else {
+        auto kern = mx_matmul_kernel<NT, kSilu, T>;
+        if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
+        return launch_k(kern, dim3(static_cast<int>(items < n_sm ? items : n_sm)), dim3(kThreads), smem,
+                        s, w, a, p);
+    }
 }
 
-template <int NT>
+template <int NT, bool kPair>
 int launch_nt(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
     if (p.dtype == MOE_F32)
-        return p.silu_mul ? launch<NT, true, float>(p, n_sm, s) : launch<NT, false, float>(p, n_sm, s);
-    return p.silu_mul ? launch<NT, true, __nv_bfloat16>(p, n_sm, s)
-                      : launch<NT, false, __nv_bfloat16>(p, n_sm, s);
+        return p.silu_mul ? launch<NT, kPair, true, float>(p, n_sm, s)
+                          : launch<NT, kPair, false, float>(p, n_sm, s);
+    return p.silu_mul ? launch<NT, kPair, true, __nv_bfloat16>(p, n_sm, s)
+                      : launch<NT, kPair, false, __nv_bfloat16>(p, n_sm, s);
 }
 
 bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -681,7 +912,7 @@ int status_address(int **out) {
 }  // namespace
 
 int launch_mx_matmul(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
-    return p.rows <= 32 * p.E ? launch_nt<32>(p, n_sm, s) : launch_nt<192>(p, n_sm, s);
+    return p.rows <= 32 * p.E ? launch_nt<32, false>(p, n_sm, s) : launch_nt<192, true>(p, n_sm, s);
 }
 
 }  // namespace moe
