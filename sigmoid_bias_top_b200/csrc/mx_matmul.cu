@@ -10,26 +10,30 @@
 //   * N = up to NT rows of one expert, rounded up to 16. An expert's rows are
 //     split into tiles of equal size, so at most 15 padded columns per tile are
 //     computed; padded columns are never stored.
-// A stage holds K = 256: 128 bytes of codes per row in the 128-byte swizzle,
-// loaded by TMA, and the two 4-byte words of scales of every row, which the
-// tensor core takes from TMEM in a layout of its own: a 512-byte block per 128
-// rows and 128 values of K, word r at (r % 32) * 16 + (r / 32) * 4. Rows start
-// anywhere, so no bulk copy can bring the scales there. Warps do: a lane loads four words, K = 512, of rows
-// lane, lane + 32, ... at once, and the transpose of its 4 x 4 words is its
-// 16-byte piece of four blocks (4-byte cp.async per word instead took 45 cycles
-// of the load unit per instruction, 900 a stage where the MMAs need 350). The
-// MMA thread copies the blocks on to TMEM (tcgen05.cp) before the stage's four
-// MMAs. Every stage has TMEM columns of its own for them: a stage is refilled
-// only after its MMAs have completed, so nothing is overwritten early.
-// Roles (480 threads): a thread of warp 0 issues TMA, one of warp 1 copies
-// scales and issues MMAs, warps 2..3 and 4..5 bring the scales of the weights
-// and of the rows, warps 6..13 drain the accumulators (two in TMEM, so that a
-// tile's epilogue runs under the next tile's MMAs), warp 14 works out the CTA's
-// items (expert, weight tile, row tile; dealt out in a fixed order), 32 at a
-// time, one a lane: divisions and searches that would cost every other role
-// 2000 cycles per item. All waits are bounded (1 s) and report a time-out in the
-// status word; the kernel then drains its copies and MMAs, frees TMEM and
-// returns.
+// A tile is one CTA's (few rows per expert) or shared by two CTAs
+// (cta_group::2): 256 weight rows, each CTA staging its own 128 of them and half
+// of the tile's rows, which the MMA reads from both; that halves what a row
+// costs each SM's shared memory, whose writes and reads bound large batches.
+// A stage holds K = 512: two TMA boxes of 256 values (128 bytes of codes) per
+// operand in the 128-byte swizzle. The scales, four 4-byte words per row and
+// stage, the tensor core takes from TMEM: column c, lane r of every 32-lane
+// quarter holds the word of row 32 c + r. TMA brings a stage's 16 bytes of every
+// row to shared memory; four warps, one per quarter, read them (rows lane, lane
+// + 32, ...) and store the words, whose transpose is a matter of register names,
+// to their quarter (tcgen05.st). What was slower: loads of the words by warps
+// (a 16-byte load of 32 rows took 150 cycles of the load unit's time, 4-byte
+// cp.async 45), and copies from shared memory to TMEM (tcgen05.cp), which run
+// in the MMAs' pipe, 30 cycles for 128 words, 360 a stage where the MMAs need 768.
+// Scale rows that TMA cannot address (K % 512, unaligned) are loaded by the four
+// warps themselves.
+// Roles (512 threads): a thread of warp 0 loads the weights' codes, one of warp
+// 15 the rows', one of warp 1 issues the MMAs, warps 2..5 bring the scales,
+// warps 6..13 drain the accumulators (two in TMEM, so that a tile's epilogue
+// runs under the next tile's MMAs), warp 14 works out the CTA's items (expert,
+// weight tile, row tile; dealt out in a fixed order), 32 at a time, one a lane:
+// divisions and searches that would cost every other role 2000 cycles per item.
+// All waits are bounded (1 s) and report a time-out in the status word; the
+// kernel then drains its copies and MMAs, frees TMEM and returns.
 #include <cooperative_groups.h>
 
 #include "mx.cuh"
@@ -40,46 +44,54 @@ namespace moe {
 namespace {
 
 constexpr int WM = 128;               // weight rows per CTA and tile
-constexpr int BK = 256;               // K per stage (128 bytes of codes per row)
+constexpr int SUBK = 256;             // K per TMA box (128 bytes of codes per row)
+constexpr int KSUB = 2;               // boxes per operand and stage
+constexpr int BK = SUBK * KSUB;       // K per stage
+constexpr int KWORDS = BK / kMxWord;  // 4-byte words of scales per row and stage
 constexpr int UK = 64;                // K per MMA
-constexpr int A_BYTES = WM * BK / 2;  // 16 KB
-constexpr int SF_BLOCK = 512;         // scales of 128 rows x 128 values
+constexpr int A_SUB = WM * SUBK / 2;  // 16 KB
+constexpr int A_BYTES = A_SUB * KSUB;
 constexpr int kEpiWarps = 8;
-constexpr int kScaleWarps = 2;        // per operand
-constexpr int kThreads = 64 + 64 * kScaleWarps + 32 * kEpiWarps + 64;
+constexpr int kScaleWarps = 4;        // one per 32-lane quarter of TMEM
+constexpr int kThreads = 32 * (4 + kScaleWarps + kEpiWarps);
 constexpr int kDeal = 32;             // items worked out at a time
-constexpr int kMaxStages = 9;
+constexpr int kMaxStages = 4;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;  // shared::cluster address in the pair's even CTA
+
+struct MxKernelParams : MxMatmulParams {
+    bool sf_tma;                  // the scales come by TMA
+};
 
 // NT: rows of a tile at most. kPair: a tile is shared by two CTAs.
 template <int NT, bool kPair>
 struct Cfg {
     static constexpr int NB = (NT + 127) / 128;        // 128-row scale blocks of the rows
+    static constexpr int R = (NT + 31) / 32;           // rows of a tile per lane
     static constexpr int B_ROWS = kPair ? NT / 2 : NT;
-    static constexpr int B_BYTES = B_ROWS * BK / 2;
-    static constexpr int SFA_BYTES = 2 * SF_BLOCK;
-    static constexpr int SFB_BYTES = 2 * NB * SF_BLOCK;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-    static constexpr int STAGES = NT <= 32 ? 9 : 5;
-    static constexpr int SF_COLS = 8 + 8 * NB;         // TMEM columns of a stage's scales
-    static constexpr int USED_COLS = 2 * NT + STAGES * SF_COLS;
+    static constexpr int B_SUB = B_ROWS * SUBK / 2;
+    static constexpr int B_BYTES = B_SUB * KSUB;
+    static constexpr int SF_BYTES = (WM + NT + 63) / 64 * 64 * 16;  // a stage's scales, 16 bytes a row
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+    static constexpr int STAGES = kPair ? 3 : 4;
+    static constexpr int SF_COLS = KWORDS * (4 + 4 * NB);  // TMEM columns of a stage's scales
+    static constexpr int SF_SLOTS = 2;                     // sets of them
+    static constexpr int USED_COLS = 2 * NT + SF_SLOTS * SF_COLS;
     static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
     static constexpr int N_STEP = kPair ? 32 : 16;     // the MMA's N is a multiple of it
     static_assert(USED_COLS <= 512 && STAGES <= kMaxStages, "TMEM");
-    static_assert(B_BYTES % 1024 == 0 && (SFA_BYTES + SFB_BYTES) % 1024 == 0, "swizzle atoms");
+    static_assert(B_SUB % 1024 == 0 && SF_BYTES % 1024 == 0, "swizzle atoms");
 };
 
 struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
     uint64_t full[kMaxStages];    // codes and scales are in place
-    uint64_t scaled[kMaxStages];  // pairs: this CTA's scales are in shared memory
-    uint64_t peer[kMaxStages];    // leader: the other CTA's are
     uint64_t empty[kMaxStages];   // the stage's MMAs are done
+    uint64_t scaled[kMaxStages];  // the stage's scales are in shared memory
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t dealt[2];            // a set of kDeal items is in place
     uint64_t taken[2];            // every role has read the set
-    uint64_t drain, copied;
+    uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -111,41 +123,20 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Arrival on the barrier at the same offset in the pair's leader. What it has to
-// order is local to this SM and done by then: TMEM reads that the caller fenced,
-// or scales in this CTA's shared memory, which their writers fenced towards the
-// async proxy and this thread has seen (an mbarrier wait in this CTA). No global
-// access has to be ordered, so there is no release to the cluster, which waits
-// for all of the SM's accesses in flight: 1300 cycles a stage.
+// Arrival on the barrier at the same offset in the pair's leader. It orders this
+// thread's TMEM accesses, which the caller has fenced, and nothing else: a
+// release to the cluster would wait for all of the thread's global accesses in
+// flight (over 700 cycles a stage).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
-// wait_bar on a barrier that threads of the other CTA arrive on.
-__device__ __forceinline__ bool wait_bar_cluster(uint64_t *bar, uint32_t parity, Ctl *ctl, int *status) {
-    const uint32_t addr = smem_u32(bar);
-    uint64_t deadline = 0;
-    for (uint32_t i = 0;; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((i & 255u) == 0u) {
-            const uint64_t now = globaltimer_ns();
-            if (deadline == 0) deadline = now + kWaitNs;
-            else if (now > deadline) break;
-        }
-    }
-    set_status(status, kStatusTimeout);
-    atomicExch(&ctl->abort, 1);
-    return false;
+// sw128_kmajor_desc in its two words; the low word moves by bytes / 16.
+constexpr uint32_t kDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) {
+    return ((saddr & 0x3FFFFu) >> 4) | 1u << 16;
 }
 
 // The instructions of one CTA, or of a pair (cta_group::2: issued by the
@@ -201,32 +192,28 @@ struct Tc {
                 "r"(smem_u32(bar))
                 : "memory");
     }
-    // 32 rows x 16 bytes of shared memory (each CTA's own) to 4 TMEM columns,
-    // repeated in the four 32-lane quarters.
-    static __device__ __forceinline__ void scales(uint32_t taddr, uint64_t desc) {
-        if constexpr (kPair)
-            asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-        else
-            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-    }
-    static __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                               uint32_t accumulate) {
+    // a, b: low words of the operands' descriptors (kDescHigh: the high word of both)
+    static __device__ __forceinline__ void mma(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
         if constexpr (kPair)
             asm volatile(
-                "{\n\t.reg .pred p;\n\t"
+                "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%1, %7};\n\t"
+                "mov.b64 y, {%2, %7};\n\t"
                 "setp.ne.b32 p, %6, 0;\n\t"
-                "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %3, [%4], [%5], p;\n\t}" ::
                     "r"(d_tmem),
-                "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+                "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHigh)
                 : "memory");
         else
             asm volatile(
-                "{\n\t.reg .pred p;\n\t"
+                "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                "mov.b64 x, {%1, %7};\n\t"
+                "mov.b64 y, {%2, %7};\n\t"
                 "setp.ne.b32 p, %6, 0;\n\t"
-                "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+                "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], x, y, %3, [%4], [%5], p;\n\t}" ::
                     "r"(d_tmem),
-                "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+                "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHigh)
                 : "memory");
     }
     // one arrival on `bar`, in both CTAs of a pair, when this thread's tcgen05 work is done
@@ -250,13 +237,6 @@ struct Tc {
             umma_commit(bar);
     }
 };
-
-// Descriptor of a 512-byte scale block: no swizzle, 8-row groups of 16-byte
-// rows 128 bytes apart, descriptor version 1.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 32 |
-           static_cast<uint64_t>(1) << 46;
-}
 
 // Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales,
 // M x N; the scales of the MMA's K = 64 are bytes 2h, 2h + 1 of their words.
@@ -336,110 +316,98 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g / (1.0f + expf(-g)) * u;
 }
 
-// Scale warp `mine` of kScaleWarps of an operand. ROWS: WM for the weights (NO =
-// outputs of the layer, o_base = first of the CTA's outputs in the tile), the
-// row tile NT for the rows (NO < 0). base: the operand's scale blocks in stage
-// 0. A chunk is K = 512, two stages; the operand's warps take the chunks in
-// turn, each with two in registers, so that their loads are in flight while
-// earlier ones are stored. Rows past the tile's end take the last one's scales:
-// their products are never stored. kVec: rows of scales are whole 16-byte words.
-template <typename C, int ROWS, bool kPaired, bool kPair, bool kVec>
-__device__ __forceinline__ void bring_scales(const MxMatmulParams &p, Ctl *ctl, const Item *items,
-                                             uint8_t *base, int NO, int o_base, int tile_outputs,
-                                             int nk, int mine) {
-    constexpr int R = (ROWS + 31) / 32;        // rows per lane
-    constexpr int NB = (ROWS + 127) / 128;     // blocks per 128 values of K
-    struct Chunk {
-        uint4 w[R];                            // four words of each of the lane's rows
-        int stages, first;                     // its stages, counted from the kernel's first
-    };
+// 32 TMEM lanes x 4 R columns: column 4 j + i of row group count R, i.e. word j
+// of the R rows of this lane in turn.
+__device__ __forceinline__ void store_words(uint32_t taddr, const uint4 (&w)[4]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(w[0].x), "r"(w[1].x), "r"(w[2].x), "r"(w[3].x), "r"(w[0].y), "r"(w[1].y), "r"(w[2].y),
+        "r"(w[3].y), "r"(w[0].z), "r"(w[1].z), "r"(w[2].z), "r"(w[3].z), "r"(w[0].w), "r"(w[1].w),
+        "r"(w[2].w), "r"(w[3].w)
+        : "memory");
+}
+__device__ __forceinline__ void store_words(uint32_t taddr, const uint4 (&w)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(w[0].x), "r"(w[1].x), "r"(w[2].x), "r"(w[3].x), "r"(w[4].x), "r"(w[5].x), "r"(w[6].x),
+        "r"(w[7].x), "r"(w[0].y), "r"(w[1].y), "r"(w[2].y), "r"(w[3].y), "r"(w[4].y), "r"(w[5].y),
+        "r"(w[6].y), "r"(w[7].y), "r"(w[0].z), "r"(w[1].z), "r"(w[2].z), "r"(w[3].z), "r"(w[4].z),
+        "r"(w[5].z), "r"(w[6].z), "r"(w[7].z), "r"(w[0].w), "r"(w[1].w), "r"(w[2].w), "r"(w[3].w),
+        "r"(w[4].w), "r"(w[5].w), "r"(w[6].w), "r"(w[7].w)
+        : "memory");
+}
+
+// A stage's 16 bytes of scale row `row` (of `rows` in the matrix), loaded word by
+// word; zeros past K.
+__device__ __forceinline__ uint4 load_words(const uint8_t *src, size_t row, int K, int kb) {
+    const uint32_t *u = reinterpret_cast<const uint32_t *>(src + row * (K / kMxBlock) + kb * 16);
+    const int left = K / kMxWord - kb * KWORDS;
+    return make_uint4(__ldg(u), left > 1 ? __ldg(u + 1) : 0u, left > 2 ? __ldg(u + 2) : 0u,
+                      left > 3 ? __ldg(u + 3) : 0u);
+}
+
+// A scale warp: the words of the CTA's 128 weight rows (first output o_base of
+// the tile's) and of the tile's rows, stage by stage, to its TMEM quarter. Rows
+// past the tile's end have any scales; their products are never stored.
+template <typename C, bool kPair, bool kSilu>
+__device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, const Item *items,
+                                             const uint8_t *smem, uint32_t tmem_sf, int NO, int o_base,
+                                             int tile_outputs, int nk) {
+    static_assert(KWORDS == 4, "a row's 16 bytes are a stage");
     const int lane = threadIdx.x & 31;
-    const bool weights = NO >= 0;
-    const uint8_t *src = weights ? p.ws : p.as;
-    const size_t pitch = static_cast<size_t>(p.K / kMxBlock);
-    const int words = p.K / kMxWord, nch = (words + 3) / 4;
+    const uint32_t taddr = tmem_sf + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
     Walk<true> walk(ctl, items, p.status);
-    const uint8_t *row[R];
-    int kc = nch, turn = 0, stage = 0;
-    bool more = true;
-
-    auto fetch = [&](Chunk &c) {
-        c.stages = 0;
-        for (; more; ++kc, turn = turn + 1 == kScaleWarps ? 0 : turn + 1) {
-            if (kc == nch) {
-                Item it;
-                more = walk.next(it);
-                if (!more) return;
-                kc = 0;
-                const uint8_t *first = src + static_cast<size_t>(weights ? it.wrow : it.t0) * pitch;
-                const int last = weights ? NO - 1 - it.wt * tile_outputs : it.rows - 1;
+    Item it;
+    int s = 0, g = 0;  // stage of the ring, and counted from the first
+    uint32_t ph = 0;
+    while (walk.next(it)) {
+        const int o_last = NO - 1 - it.wt * tile_outputs;
+        for (int kb = 0; kb < nk; ++kb) {
+            uint4 a[4], b[4 * C::NB];
+            if (p.sf_tma) {
+                if (!wait_bar(&ctl->scaled[s], ph, ctl, p.status)) return;
+                const uint8_t *sf = smem + s * C::STAGE_BYTES + A_BYTES + C::B_BYTES + lane * 16;
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    // paired: 16 gate rows and their 16 up rows in turn
-                    int o = weights ? o_base + (kPaired ? i * 16 + (lane & 15) : i * 32 + lane) : i * 32 + lane;
-                    o = min(o, last) + (kPaired && lane >= 16 ? NO : 0);
-                    row[i] = first + static_cast<size_t>(o) * pitch;
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const uint4 *>(sf + i * 512);
+#pragma unroll
+                for (int i = 0; i < 4 * C::NB; ++i)
+                    b[i] = i < C::R ? *reinterpret_cast<const uint4 *>(sf + WM * 16 + i * 512) : b[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // gate/up: 16 gate rows and their 16 up rows in turn
+                    const int o = min(o_base + (kSilu ? i * 16 + (lane & 15) : i * 32 + lane), o_last);
+                    a[i] = load_words(p.ws, static_cast<size_t>(it.wrow) + o + (kSilu && lane >= 16 ? NO : 0),
+                                      p.K, kb);
                 }
+#pragma unroll
+                for (int i = 0; i < 4 * C::NB; ++i)
+                    b[i] = i < C::R ? load_words(p.as, static_cast<size_t>(it.t0) + min(i * 32 + lane, it.rows - 1),
+                                                 p.K, kb)
+                                    : b[0];
             }
-            const int n = min(2, nk - 2 * kc);
-            if (turn == mine) {
-                c.stages = n;
-                c.first = stage;
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    if constexpr (kVec) {
-                        c.w[i] = __ldg(reinterpret_cast<const uint4 *>(row[i] + kc * 16));
-                    } else {
-                        const uint32_t *u = reinterpret_cast<const uint32_t *>(row[i] + kc * 16);
-                        const int left = words - kc * 4;
-                        c.w[i].x = __ldg(u);
-                        c.w[i].y = left > 1 ? __ldg(u + 1) : 0u;
-                        c.w[i].z = left > 2 ? __ldg(u + 2) : 0u;
-                        c.w[i].w = left > 3 ? __ldg(u + 3) : 0u;
-                    }
-                }
-                stage += n;
-                ++kc;
-                turn = turn + 1 == kScaleWarps ? 0 : turn + 1;
+            // the MMAs that read the slot's last scales are done
+            const int o = g - C::SF_SLOTS;
+            if (o >= 0 && !wait_bar(&ctl->empty[o % C::STAGES], static_cast<uint32_t>(o / C::STAGES) & 1u,
+                                    ctl, p.status))
                 return;
-            }
-            stage += n;
-        }
-    };
-    auto put = [&](const Chunk &c) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (h >= c.stages) break;
-            const int s = (c.first + h) % C::STAGES;
-            const uint32_t ph = static_cast<uint32_t>((c.first + h) / C::STAGES) & 1u;
-            if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) return false;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint32_t v[4];  // word 2h + j of the lane's four rows of the block
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 &w = c.w[4 * b + i < R ? 4 * b + i : R - 1];
-                        v[i] = h == 0 ? (j == 0 ? w.x : w.y) : (j == 0 ? w.z : w.w);
-                    }
-                    *reinterpret_cast<uint4 *>(base + s * C::STAGE_BYTES + (j * NB + b) * SF_BLOCK + lane * 16) =
-                        make_uint4(v[0], v[1], v[2], v[3]);
-                }
-            fence_proxy_async_smem();  // before the tensor core's copy reads them
+            tc_fence_after();
+            const uint32_t to = taddr + static_cast<uint32_t>((g % C::SF_SLOTS) * C::SF_COLS);
+            store_words(to, a);
+            store_words(to + 4 * KWORDS, b);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(kPair ? &ctl->scaled[s] : &ctl->full[s]);
+            if (lane == 0) {
+                if constexpr (kPair) mbar_arrive_leader(&ctl->full[s]);
+                else mbar_arrive(&ctl->full[s]);
+            }
+            ++g;
+            if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
-        return true;
-    };
-
-    Chunk c0, c1;
-    fetch(c0);
-    for (;;) {
-        fetch(c1);
-        if (c0.stages == 0 || !put(c0)) break;
-        fetch(c0);
-        if (c1.stages == 0 || !put(c1)) break;
     }
 }
 
@@ -520,16 +488,18 @@ struct Drain {
             __syncwarp();
             constexpr int kPieces = kOutputs / 8;       // 16-byte pieces of a row
             const int col = f0 + (lane % kPieces) * 8;  // NO % 16 == 0: all 8 outputs or none
+            uint4 v[kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                             : "r"(stage + (i * 32 + lane) / kPieces * kPitch + (lane % kPieces) * 16)
+                             : "memory");
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int r = (i * 32 + lane) / kPieces;
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(stage + r * kPitch + (lane % kPieces) * 16)
-                             : "memory");
                 if (r < lim && col < NO)
-                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(r) * NO + col) = v;
+                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(r) * NO + col) = v[i];
             }
             __syncwarp();  // the staging rows are read before the next chunk's are written
         } else {
@@ -553,24 +523,10 @@ __device__ __forceinline__ int mma_n(const Item &it) {
     return (it.rows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
 }
 
-// A stage's scale blocks (shared address sf) to its TMEM columns; two: the rows
-// fill more than one block.
-template <typename C, bool kPair>
-__device__ __forceinline__ void copy_scales(uint32_t sf, uint32_t taddr, bool two) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        Tc<kPair>::scales(taddr + 4 * j, scale_desc(sf + j * SF_BLOCK));
-#pragma unroll
-        for (int b = 0; b < C::NB; ++b)
-            if (b == 0 || two)
-                Tc<kPair>::scales(taddr + 8 + 4 * (j * C::NB + b),
-                                  scale_desc(sf + C::SFA_BYTES + (j * C::NB + b) * SF_BLOCK));
-    }
-}
-
 template <int NT, bool kPair, bool kSilu, typename T>
 __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUtensorMap &tmA,
-                                               const MxMatmulParams &p) {
+                                               const CUtensorMap &tmSW, const CUtensorMap &tmSA,
+                                               const MxKernelParams &p) {
     using C = Cfg<NT, kPair>;
     using X = Tc<kPair>;
     constexpr int kCtas = kPair ? 2 : 1;
@@ -589,22 +545,19 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            // the TMA thread, and a scale warp of each operand or, for pairs, the
-            // commit of the scales' copies
-            mbar_init(&ctl->full[s], kPair ? 2 : 3);
-            mbar_init(&ctl->scaled[s], 2);  // a scale warp of each operand
-            mbar_init(&ctl->peer[s], 1);
+            // the two TMA threads (of the leader), the scale warps (of both CTAs)
+            mbar_init(&ctl->full[s], 2 + kCtas * kScaleWarps);
+            mbar_init(&ctl->scaled[s], 2);  // the two TMA threads
             mbar_init(&ctl->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
             mbar_init(&ctl->tempty[b], kCtas * kEpiWarps);
             mbar_init(&ctl->dealt[b], 1);
-            // TMA, scale and epilogue warps; MMA thread of the leader, copy threads of pairs
-            mbar_init(&ctl->taken[b], 1 + 2 * kScaleWarps + kEpiWarps + (kPair ? leader ? 2 : 1 : 1));
+            // every role but the dealer; one CTA of a pair has no MMA thread
+            mbar_init(&ctl->taken[b], 2 + kScaleWarps + kEpiWarps + (leader ? 1 : 0));
         }
         mbar_init(&ctl->drain, 1);
-        mbar_init(&ctl->copied, 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
@@ -612,6 +565,10 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmA);
+        if (p.sf_tma) {
+            tma_prefetch_desc(&tmSW);
+            tma_prefetch_desc(&tmSA);
+        }
     }
     pdl_trigger();
     pdl_wait();
@@ -652,9 +609,10 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     const int nk = (p.K + BK - 1) / BK;
     const int total = mts[E] * NW;  // out fits in memory: far below 2^31
 
-    if (warp == 0) {
+    if (warp == 0 || warp == kThreads / 32 - 1) {
         if (elect_one()) {
-            // ------------------------- TMA producer -------------------------
+            // ----------- TMA producers: the weights', the rows' -----------
+            const bool weights = warp == 0;
             int s = 0;
             uint32_t ph = 0;
             bool issued[C::STAGES];
@@ -669,11 +627,23 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) { ok = false; break; }
                     uint8_t *sa = smem + s * C::STAGE_BYTES;
-                    if (leader) mbar_arrive_expect_tx(&ctl->full[s], kCtas * (A_BYTES + C::B_BYTES));
-                    // the maps count two-byte columns: 64 of them are K = 256
-                    if (kSilu) X::load_4d(sa, &tmW, kb * 64, wrow / 16, &ctl->full[s]);
-                    else X::load_2d(sa, &tmW, kb * 64, wrow, &ctl->full[s]);
-                    X::load_2d(sa + A_BYTES, &tmA, kb * 64, trow, &ctl->full[s]);
+                    if (leader) mbar_arrive_expect_tx(&ctl->full[s], kCtas * (weights ? A_BYTES : C::B_BYTES));
+                    // the maps count two-byte columns: 64 of them are a box; what lies
+                    // past K arrives as zeros
+#pragma unroll
+                    for (int j = 0; j < KSUB; ++j) {
+                        const int x = (kb * KSUB + j) * 64;
+                        if (!weights) X::load_2d(sa + A_BYTES + j * C::B_SUB, &tmA, x, trow, &ctl->full[s]);
+                        else if (kSilu) X::load_4d(sa + j * A_SUB, &tmW, x, wrow / 16, &ctl->full[s]);
+                        else X::load_2d(sa + j * A_SUB, &tmW, x, wrow, &ctl->full[s]);
+                    }
+                    if (p.sf_tma) {  // every CTA its own weight rows' scales and all of the tile's rows'
+                        uint8_t *sf = sa + A_BYTES + C::B_BYTES;
+                        mbar_arrive_expect_tx(&ctl->scaled[s], (weights ? WM : NT) * 16);
+                        if (!weights) tma_load_2d(sf + WM * 16, &tmSA, kb * 8, it.t0, &ctl->scaled[s]);
+                        else if (kSilu) Tc<false>::load_4d(sf, &tmSW, kb * 8, wrow / 16, &ctl->scaled[s]);
+                        else tma_load_2d(sf, &tmSW, kb * 8, wrow, &ctl->scaled[s]);
+                    }
                     issued[s] = true;
                     issued_parity[s] = ph;
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
@@ -683,14 +653,18 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             if (!ok || aborted(ctl)) {  // let the other roles leave and our own copies land
                 atomicExch(&ctl->abort, 1);
                 const uint64_t dl = globaltimer_ns() + kWaitNs;
-                for (int i = 0; leader && i < C::STAGES; ++i)
-                    if (issued[i]) mbar_wait(&ctl->full[i], issued_parity[i], dl);
+                for (int i = 0; i < C::STAGES; ++i)
+                    if (issued[i]) {
+                        if (leader) mbar_wait(&ctl->full[i], issued_parity[i], dl);
+                        if (p.sf_tma) mbar_wait(&ctl->scaled[i], issued_parity[i], dl);
+                    }
             }
         }
     } else if (warp == 1) {
         if (leader && elect_one()) {
             // ----------------------------- MMA ------------------------------
-            int s = 0, tile = 0;
+            const uint32_t desc0 = desc_low(smem_u32(smem));
+            int s = 0, tile = 0, slot = 0;
             uint32_t ph = 0;
             bool any = false;
             Walk<false> walk(ctl, items, p.status);
@@ -698,9 +672,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             for (; walk.next(it); ++tile) {
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
-                if (kPair ? !wait_bar_cluster(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)
-                          : !wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status))
-                    break;
+                if (!wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * NT);
                 const int n = mma_n<C>(it);
@@ -709,16 +681,16 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!wait_bar(&ctl->full[s], ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t b0 = a0 + A_BYTES;
-                    const uint32_t ta = tmem_sf + static_cast<uint32_t>(s * C::SF_COLS), tb = ta + 8;
-                    if constexpr (!kPair) copy_scales<C, kPair>(b0 + C::B_BYTES, ta, n > 128);
+                    const uint32_t a0 = desc0 + static_cast<uint32_t>(s) * (C::STAGE_BYTES / 16);
+                    const uint32_t b0 = a0 + A_BYTES / 16;
+                    const uint32_t ta = tmem_sf + static_cast<uint32_t>(slot * C::SF_COLS);
+                    const uint32_t tb = ta + 4 * KWORDS;
 #pragma unroll
                     for (int kk = 0; kk < BK / UK; ++kk)
-                        X::mma(d_tmem, sw128_kmajor_desc(a0 + kk * UK / 2),
-                               sw128_kmajor_desc(b0 + kk * UK / 2), idesc[kk & 1],
-                               ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1),
-                               (kb | kk) != 0 ? 1u : 0u);
+                        X::mma(d_tmem, a0 + ((kk >> 2) * A_SUB + (kk & 3) * (UK / 2)) / 16,
+                               b0 + ((kk >> 2) * C::B_SUB + (kk & 3) * (UK / 2)) / 16, idesc[kk & 1],
+                               ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
+                    if (++slot == C::SF_SLOTS) slot = 0;
                     any = true;
                     X::commit(&ctl->empty[s]);
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
@@ -731,51 +703,9 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 mbar_wait(&ctl->drain, 0, globaltimer_ns() + kWaitNs);
             }
         }
-    } else if (warp < 2 + 2 * kScaleWarps) {
+    } else if (warp < 2 + kScaleWarps) {
         // ---------------------------- scales ----------------------------
-        const bool weights = warp < 2 + kScaleWarps;
-        const int mine = (warp - 2) % kScaleWarps;
-        uint8_t *sf = smem + A_BYTES + C::B_BYTES;
-        const bool vec = p.K % 512 == 0 &&
-                         (reinterpret_cast<uintptr_t>(weights ? p.ws : p.as) & 15u) == 0;
-        if (weights && vec)
-            bring_scales<C, WM, kSilu, kPair, true>(p, ctl, items, sf, NO, half * kCtaOutputs, kOutputs, nk, mine);
-        else if (weights)
-            bring_scales<C, WM, kSilu, kPair, false>(p, ctl, items, sf, NO, half * kCtaOutputs, kOutputs, nk, mine);
-        else if (vec)
-            bring_scales<C, NT, false, kPair, true>(p, ctl, items, sf + C::SFA_BYTES, -1, 0, 0, nk, mine);
-        else
-            bring_scales<C, NT, false, kPair, false>(p, ctl, items, sf + C::SFA_BYTES, -1, 0, 0, nk, mine);
-    } else if (warp == kThreads / 32 - 1) {
-        if (kPair && elect_one()) {
-            // ---- pairs: scales on to TMEM by the leader, told by the other CTA ----
-            int s = 0;
-            uint32_t ph = 0;
-            bool any = false, ok = true;
-            Walk<false> walk(ctl, items, p.status);
-            Item it;
-            while (ok && walk.next(it)) {
-                const bool two = mma_n<C>(it) > 128;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(&ctl->scaled[s], ph, ctl, p.status)) { ok = false; break; }
-                    if (leader) {
-                        if (!wait_bar_cluster(&ctl->peer[s], ph, ctl, p.status)) { ok = false; break; }
-                        tc_fence_after();
-                        copy_scales<C, kPair>(smem_u32(smem + s * C::STAGE_BYTES) + A_BYTES + C::B_BYTES,
-                                              tmem_sf + static_cast<uint32_t>(s * C::SF_COLS), two);
-                        X::commit_here(&ctl->full[s]);
-                        any = true;
-                    } else {
-                        mbar_arrive_leader(&ctl->peer[s]);
-                    }
-                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
-                }
-            }
-            if (any) {  // no copy is in flight when the kernel ends
-                X::commit_here(&ctl->copied);
-                mbar_wait(&ctl->copied, 0, globaltimer_ns() + kWaitNs);
-            }
-        }
+        bring_scales<C, kPair, kSilu>(p, ctl, items, smem, tmem_sf, NO, half * kCtaOutputs, kOutputs, nk);
     } else if (warp == kThreads / 32 - 2) {
         // ------------------------- item dealer --------------------------
         for (int c = 0;; ++c) {
@@ -793,7 +723,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     } else {
         // --------------------------- epilogue ---------------------------
         const int q = warp & 3;                   // TMEM lane quarter of this warp
-        const int ew = warp - 2 - 2 * kScaleWarps;
+        const int ew = warp - 2 - kScaleWarps;
         const int c_first = (ew >> 2) * 32;       // its 32-column chunks, every second
         const uint32_t stage = smem_u32(stages_out) + ew * Drain<kSilu, T>::kStage;
         T *out = static_cast<T *>(p.out);
@@ -834,15 +764,18 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
 template <int NT, bool kSilu, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_matmul_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                     MxMatmulParams p) {
-    mx_matmul_body<NT, false, kSilu, T>(tmW, tmA, p);
+                     const __grid_constant__ CUtensorMap tmSW,
+                     const __grid_constant__ CUtensorMap tmSA, MxKernelParams p) {
+    mx_matmul_body<NT, false, kSilu, T>(tmW, tmA, tmSW, tmSA, p);
 }
 
 template <int NT, bool kSilu, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmW,
-                          const __grid_constant__ CUtensorMap tmA, MxMatmulParams p) {
-    mx_matmul_body<NT, true, kSilu, T>(tmW, tmA, p);
+                          const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmSW,
+                          const __grid_constant__ CUtensorMap tmSA, MxKernelParams p) {
+    mx_matmul_body<NT, true, kSilu, T>(tmW, tmA, tmSW, tmSA, p);
 }
 
 // Device-side failures of calls without a context (moe_mx_status).
@@ -863,16 +796,59 @@ int resident_pairs(const void *kern, size_t smem, int n_sm) {
     return n < n_sm / 2 ? n : n_sm / 2;
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Map of a scale matrix [rows][pitch bytes] in two-byte columns: a box is 16
+// bytes of box_rows rows, or, with up_offset, of 4 groups of 16 rows and the 16
+// rows up_offset further each (as tc_encode_pair_4d has it for the codes).
+int encode_scales(CUtensorMap *m, const void *base, uint64_t rows, uint64_t pitch, uint32_t box_rows,
+                  uint64_t up_offset) {
+    static void *fn = nullptr;
+    if (!fn) {
+        cudaDriverEntryPointQueryResult q;
+        void *ptr = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !ptr)
+            return MOE_ERR_CUDA;
+        fn = ptr;
+    }
+    const bool paired = up_offset != 0;
+    const cuuint64_t dims[4] = {pitch / 2, paired ? 16 : rows, 2, paired ? (rows - up_offset) / 16 : 0};
+    const cuuint64_t strides[3] = {pitch, pitch * up_offset, pitch * 16};
+    const cuuint32_t box[4] = {8, paired ? 16 : box_rows, 2, 4};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = reinterpret_cast<EncodeTiledFn>(fn)(
+        m, CU_TENSOR_MAP_DATA_TYPE_UINT16, paired ? 4 : 2, const_cast<void *>(base), dims, strides, box,
+        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
 template <int NT, bool kPair, bool kSilu, typename T>
-int launch(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
+int launch(const MxMatmulParams &args, int n_sm, cudaStream_t s) {
     using C = Cfg<NT, kPair>;
-    CUtensorMap w, a;
+    CUtensorMap w, a, sw = {}, sa = {};
+    MxKernelParams p;
+    static_cast<MxMatmulParams &>(p) = args;
+    // TMA wants 16-byte row pitches and addresses
+    p.sf_tma = p.K % BK == 0 && aligned(p.ws, 16) && aligned(p.as, 16);
     int rc;
     const uint64_t wrows = static_cast<uint64_t>(p.E) * p.N;
     if (kSilu) rc = tc_encode_pair_4d(&w, p.w, wrows, p.K / 4, p.N / 2);
     else rc = tc_encode_2d(&w, p.w, wrows, p.K / 4, WM);
     if (rc != MOE_OK) return rc;
     if ((rc = tc_encode_2d(&a, p.a, p.rows, p.K / 4, C::B_ROWS)) != MOE_OK) return rc;
+    if (p.sf_tma) {
+        const uint64_t pitch = p.K / kMxBlock;
+        if ((rc = encode_scales(&sw, p.ws, wrows, pitch, WM, kSilu ? p.N / 2 : 0)) != MOE_OK ||
+            (rc = encode_scales(&sa, p.as, p.rows, pitch, NT, 0)) != MOE_OK)
+            return rc;
+    }
     const size_t smem = 1024 + C::STAGES * C::STAGE_BYTES + kEpiWarps * Drain<kSilu, T>::kStage +
                         sizeof(Ctl) + 2 * kDeal * sizeof(Item) + 2 * (p.E + 1) * sizeof(int32_t);
     // no more CTAs than there can be items
@@ -884,12 +860,12 @@ int launch(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
         static int resident = 0;  // per kernel, for the device model of the process
         if (resident == 0) resident = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
         const int pairs = static_cast<int>(items < resident ? items : resident);
-        return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, w, a, p);
+        return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, w, a, sw, sa, p);
     } else {
         auto kern = mx_matmul_kernel<NT, kSilu, T>;
         if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
         return launch_k(kern, dim3(static_cast<int>(items < n_sm ? items : n_sm)), dim3(kThreads), smem,
-                        s, w, a, p);
+                        s, w, a, sw, sa, p);
     }
 }
 
@@ -901,8 +877,6 @@ int launch_nt(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
     return p.silu_mul ? launch<NT, kPair, true, __nv_bfloat16>(p, n_sm, s)
                       : launch<NT, kPair, false, __nv_bfloat16>(p, n_sm, s);
 }
-
-bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int status_address(int **out) {
     return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_mx_status) == cudaSuccess ? MOE_OK
