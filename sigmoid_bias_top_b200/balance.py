@@ -18,7 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import MOE_BF16, MOE_F32, _check, lib as _moe_lib
-from .mx import _On
+from .mx import _On, _here, _raw_stream
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -63,36 +63,36 @@ class _BalanceLoss(torch.autograd.Function):
         k, dev = idx.shape[1], logits.device
         B = 1 if seq_offsets is None else seq_offsets.numel() - 1
         L = lib()
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        scale = torch.empty((), dtype=torch.float32, device=dev)
+        both = torch.empty(2, dtype=torch.float32, device=dev)   # loss, scale
         counts = torch.empty(B, E, dtype=torch.int32, device=dev)
         prob = torch.empty(B, E, dtype=torch.float32, device=dev)
-        with _On(dev, None) as s:
-            ws = torch.empty(L.moe_balance_workspace(n, E, B), dtype=torch.uint8, device=dev)
-            _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype],
-                                         _ld(logits), idx.data_ptr(), _ptr(seq_offsets), n, E,
-                                         k, B, coef, eps, ws.data_ptr(), loss.data_ptr(),
-                                         counts.data_ptr(), prob.data_ptr(), scale.data_ptr(), s),
-                   "moe_balance_forward")
-        ctx.save_for_backward(logits, counts, scale, seq_offsets)
+        ws = torch.empty(L.moe_balance_workspace(n, E, B), dtype=torch.uint8, device=dev)
+        ptr = both.data_ptr()
+        _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
+                                     idx.data_ptr(), _ptr(seq_offsets), n, E, k, B, coef, eps,
+                                     ws.data_ptr(), ptr, counts.data_ptr(), prob.data_ptr(),
+                                     ptr + 4, _raw_stream(dev.index)), "moe_balance_forward")
+        ctx.save_for_backward(logits, counts, both, seq_offsets)
         ctx.k, ctx.eps = k, eps
         ctx.mark_non_differentiable(counts, prob)
-        return loss, counts, prob
+        ctx.set_materialize_grads(False)
+        return both[0], counts, prob
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_loss, _counts, _prob):
-        logits, counts, scale, seq_offsets = ctx.saved_tensors
+        if grad_loss is None:
+            return None, None, None, None, None
+        logits, counts, both, seq_offsets = ctx.saved_tensors
         n, E = logits.shape
-        grad = torch.empty(n, E, dtype=logits.dtype, device=logits.device)
-        grad_loss = grad_loss.float()
-        with _On(logits.device, None) as s:
-            _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype],
-                                              _ld(logits), counts.data_ptr(),
-                                              _ptr(seq_offsets), scale.data_ptr(),
-                                              grad_loss.data_ptr(), n, E, ctx.k, counts.shape[0],
-                                              ctx.eps, grad.data_ptr(), s),
-                   "moe_balance_backward")
+        dev = logits.device
+        grad = torch.empty(n, E, dtype=logits.dtype, device=dev)
+        # autograd runs this with the forward call's device and stream current
+        _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
+                                          counts.data_ptr(), _ptr(seq_offsets),
+                                          both.data_ptr() + 4, grad_loss.data_ptr(), n, E, ctx.k,
+                                          counts.shape[0], ctx.eps, grad.data_ptr(),
+                                          _raw_stream(dev.index)), "moe_balance_backward")
         return grad, None, None, None, None
 
 
@@ -110,14 +110,17 @@ def balance_loss(logits, idx, seq_offsets: Optional[torch.Tensor] = None, coef: 
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be an [n, E] CUDA tensor")
     n, E = logits.shape
-    if E > 1 and logits.stride(1) != 1 or _ld(logits) < E:
-        logits = logits.contiguous()
+    device = logits.device
     if (idx.dtype != torch.int32 or idx.dim() != 2 or idx.shape[0] != n
-            or not idx.is_contiguous() or idx.device != logits.device):
-        raise ValueError(f"idx must be a contiguous int32 ({n}, k) tensor on {logits.device}")
+            or not idx.is_contiguous() or idx.device != device):
+        raise ValueError(f"idx must be a contiguous int32 ({n}, k) tensor on {device}")
     if seq_offsets is not None and (
             seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 2
-            or not seq_offsets.is_contiguous() or seq_offsets.device != logits.device):
-        raise ValueError("seq_offsets must be a contiguous int32 (B + 1,) tensor on "
-                         f"{logits.device}")
+            or not seq_offsets.is_contiguous() or seq_offsets.device != device):
+        raise ValueError(f"seq_offsets must be a contiguous int32 (B + 1,) tensor on {device}")
+    if not _here(device, None):
+        with _On(device, None):
+            return balance_loss(logits, idx, seq_offsets, coef, eps)
+    if E > 1 and logits.stride(1) != 1 or _ld(logits) < E:
+        logits = logits.contiguous()
     return Balance(*_BalanceLoss.apply(logits, idx, seq_offsets, float(coef), float(eps)))

@@ -49,47 +49,55 @@ def lib():
     return L
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device, without building a Stream
+
+
 class _On:
     """Makes the device of the tensors and the stream to launch on current (the
     given stream, or that device's current one), so that copies and outputs made
-    inside belong to that stream too."""
+    inside belong to that stream too. Only needed where _here says no."""
 
     def __init__(self, device, stream):
-        self.inner = None
-        if stream is not None:
+        if stream is None:
+            self.inner = torch.cuda.device(device)
+        else:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.inner = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.inner = torch.cuda.device(device)
-        self.device = device
 
     def __enter__(self):
-        if self.inner is not None:
-            self.inner.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        self.inner.__enter__()
 
     def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
+        self.inner.__exit__(*exc)
 
 
-def _mx(name: str, q: MxTensor, dims) -> None:
+def _here(device, stream) -> bool:
+    """Whether a launch needs neither another device nor another stream."""
+    return stream is None and device.index == _current_device()
+
+
+def _mx(name: str, q: MxTensor, least: int, most: int):
+    """Checks a quantised argument; returns (codes, scales, its device)."""
     c, s = q
     for what, t in (("codes", c), ("scales", s)):
         if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_cuda:
             raise TypeError(f"{name}.{what} must be a uint8 CUDA tensor")
         if not t.is_contiguous():
             raise ValueError(f"{name}.{what} must be contiguous")
-    if (c.dim() not in dims or c.shape[:-1] != s.shape[:-1] or c.shape[-1] != 16 * s.shape[-1]
-            or c.device != s.device):
+    cs, ss = c.shape, s.shape
+    device = c.device
+    if (not least <= len(cs) <= most or cs[:-1] != ss[:-1] or cs[-1] != 16 * ss[-1]
+            or device != s.device):
         raise ValueError(f"{name}: codes [..., K/2] and scales [..., K/32] of one shape and device, "
-                         f"got {tuple(c.shape)} and {tuple(s.shape)}")
+                         f"got {tuple(cs)} and {tuple(ss)}")
+    return c, s, device
 
 
 def _out(out: Optional[torch.Tensor], shape, dtype, device):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     if (out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device
             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {dtype} {tuple(shape)} tensor on {device}")
@@ -99,47 +107,53 @@ def _out(out: Optional[torch.Tensor], shape, dtype, device):
 def quantize(x: torch.Tensor, out: Optional[MxTensor] = None, stream=None) -> MxTensor:
     """MXFP4 of x [..., K] (f32 or bf16, K % 32 == 0). A matrix may have strided
     rows; other layouts that the kernel cannot read in place are copied first."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+    dt = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    if dt is None:
         raise TypeError("x must be a float32 or bfloat16 tensor")
-    if not x.is_cuda or x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % BLOCK:
+    shape = x.shape
+    if not x.is_cuda or len(shape) < 1 or shape[-1] == 0 or shape[-1] % BLOCK:
         raise ValueError("x must be a [..., K] CUDA tensor with K a multiple of 32")
-    K = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    with _On(x.device, stream) as s:
-        ld = K
-        if not x.is_contiguous():
-            if x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K and \
-                    x.stride(0) * x.element_size() % 16 == 0:
-                ld = x.stride(0)
-            else:
-                x = x.contiguous()
-        if x.data_ptr() % 16:
-            x, ld = x.clone(memory_format=torch.contiguous_format), K
-        if out is None:
-            out = MxTensor(torch.empty(*lead, K // 2, dtype=torch.uint8, device=x.device),
-                           torch.empty(*lead, K // BLOCK, dtype=torch.uint8, device=x.device))
+    device = x.device
+    if not _here(device, stream):
+        with _On(device, stream):
+            return quantize(x, out)
+    K = ld = shape[-1]
+    if not x.is_contiguous():
+        if len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= K and \
+                x.stride(0) * x.element_size() % 16 == 0:
+            ld = x.stride(0)
         else:
-            out = MxTensor(_out(out[0], (*lead, K // 2), torch.uint8, x.device),
-                           _out(out[1], (*lead, K // BLOCK), torch.uint8, x.device))
-        _check(lib().moe_mx_quantize(x.data_ptr(), _DTYPES[x.dtype], x.numel() // K, K, ld,
-                                     out.codes.data_ptr(), out.scales.data_ptr(), s),
-               "moe_mx_quantize")
-    return out
+            x = x.contiguous()
+    ptr = x.data_ptr()
+    if ptr % 16:
+        x, ld = x.clone(memory_format=torch.contiguous_format), K
+        ptr = x.data_ptr()
+    lead = shape[:-1]
+    given = (None, None) if out is None else out
+    codes = _out(given[0], (*lead, K // 2), torch.uint8, device)
+    scales = _out(given[1], (*lead, K // BLOCK), torch.uint8, device)
+    _check(lib().moe_mx_quantize(ptr, dt, x.numel() // K, K, ld, codes.data_ptr(),
+                                 scales.data_ptr(), _raw_stream(device.index)), "moe_mx_quantize")
+    return MxTensor(codes, scales)
 
 
 def dequantize(q: MxTensor, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The values of q, [..., K] in dtype (bf16 holds those of quantize exactly)."""
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError("dtype must be float32 or bfloat16")
-    _mx("q", q, range(1, 9))
-    codes, scales = q
-    K = codes.shape[-1] * 2
+    codes, scales, device = _mx("q", q, 1, 8)
+    shape = codes.shape
+    K = shape[-1] * 2
     if K == 0:
         raise ValueError("q has no columns")
-    with _On(codes.device, stream) as s:
-        out = _out(out, (*codes.shape[:-1], K), dtype, codes.device)
-        _check(lib().moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.numel() // K, K,
-                                       out.data_ptr(), _DTYPES[dtype], s), "moe_mx_dequantize")
+    if not _here(device, stream):
+        with _On(device, stream):
+            return dequantize(q, dtype, out)
+    out = _out(out, (*shape[:-1], K), dtype, device)
+    _check(lib().moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.numel() // K, K,
+                                   out.data_ptr(), dt, _raw_stream(device.index)),
+           "moe_mx_dequantize")
     return out
 
 
@@ -153,27 +167,29 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
     out). silu_mul: w holds the gate rows, then the up rows, and the result is
     silu(gate) * up, [rows, N / 2]. K % 128 == 0, N % 16 == 0 (32 with
     silu_mul), E <= 256. Sums are fp32, rounded once to dtype (bf16 or f32)."""
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError("dtype must be float32 or bfloat16")
-    _mx("a", a, (2,))
-    _mx("w", w, (2,) if offsets is None else (3,))
-    rows, K = a.shape
-    E = 1 if offsets is None else w.codes.shape[0]
-    N = w.codes.shape[-2]
-    if w.shape[-1] != K or w.codes.device != a.codes.device:
-        raise ValueError(f"w must hold rows of {K} values on {a.codes.device}")
-    if offsets is not None and (offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,)
-                                or not offsets.is_contiguous()
-                                or offsets.device != a.codes.device):
-        raise ValueError(f"offsets must be a contiguous int32 ({E + 1},) tensor on "
-                         f"{a.codes.device}")
-    with _On(a.codes.device, stream) as s:
-        out = _out(out, (rows, N // 2 if silu_mul else N), dtype, a.codes.device)
-        _check(lib().moe_mx_matmul(a.codes.data_ptr(), a.scales.data_ptr(), w.codes.data_ptr(),
-                                   w.scales.data_ptr(),
-                                   None if offsets is None else offsets.data_ptr(), rows, K, E, N,
-                                   int(silu_mul), out.data_ptr(), _DTYPES[dtype], s),
-               "moe_mx_matmul")
+    ac, as_, device = _mx("a", a, 2, 2)
+    wc, ws, w_device = _mx("w", w, 2, 2) if offsets is None else _mx("w", w, 3, 3)
+    rows, half = ac.shape
+    N = wc.shape[-2]
+    if wc.shape[-1] != half or w_device != device:
+        raise ValueError(f"w must hold rows of {2 * half} values on {device}")
+    E, offs = 1, None
+    if offsets is not None:
+        E = wc.shape[0]
+        if (offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,)
+                or not offsets.is_contiguous() or offsets.device != device):
+            raise ValueError(f"offsets must be a contiguous int32 ({E + 1},) tensor on {device}")
+        offs = offsets.data_ptr()
+    if not _here(device, stream):
+        with _On(device, stream):
+            return matmul(a, w, offsets, silu_mul, dtype, out)
+    out = _out(out, (rows, N // 2 if silu_mul else N), dtype, device)
+    _check(lib().moe_mx_matmul(ac.data_ptr(), as_.data_ptr(), wc.data_ptr(), ws.data_ptr(), offs,
+                               rows, 2 * half, E, N, 1 if silu_mul else 0, out.data_ptr(), dt,
+                               _raw_stream(device.index)), "moe_mx_matmul")
     return out
 
 
