@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kFinishThreads = 1024;
 constexpr int kV = 8;               // experts per lane
 constexpr int kMinChunk = 8;        // tokens
 constexpr int kMaxChunks = 148 * 4; // chunks of a large batch: four CTAs an SM
@@ -111,6 +112,9 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
     }
 }
 
+// The exponential and the reciprocal are the fast ones: 2^-22 relative plus
+// |v| 2^-23 from the rounded product with log2(e), no more than what an fp32 sum
+// over the experts loses, and half the kernels' time.
 // v = sigmoid(v) per value; returns the row's sum of scores plus eps. slope, if
 // given, gets sigmoid's derivative: with t = exp(-|v|) it is t / (1 + t)^2,
 // which keeps its relative accuracy where 1 - s would cancel.
@@ -119,8 +123,8 @@ __device__ __forceinline__ float scores(float (&v)[kV], float eps, float *slope 
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-        const float t = expf(-fabsf(v[i]));
-        const float r = 1.0f / (1.0f + t);
+        const float t = __expf(-fabsf(v[i]));
+        const float r = __fdividef(1.0f, 1.0f + t);
         v[i] = v[i] < 0.f ? t * r : r;   // a NaN stays one through t
         if (slope) slope[i] = t * r * r;
         sum += v[i];
@@ -153,16 +157,24 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(FwdParams p) 
 #pragma unroll
         for (int i = 0; i < kV; ++i) acc[i] = 0.f;
         __syncthreads();
-        for (int r0 = t + warp * G; r0 < stop; r0 += kWarps * G) {
-            const int r = r0 + grp;
-            float v[kV];
-            load_logits<kF32>(p.logits, (r < stop ? r : r0) * p.ld, e0, p.E, p.vec, v);
-            const float total = scores<TPR>(v, p.eps);
-            if (r < stop) {
-                // eps may be 0 and every score may have underflowed: no share then
-                const float inv = total == 0.f ? 0.f : 1.0f / total;
+        // the rows of two steps are loaded before the first is worked on
+        for (int r0 = t + warp * G; r0 < stop; r0 += 2 * kWarps * G) {
+            float v[2][kV];
 #pragma unroll
-                for (int i = 0; i < kV; ++i) acc[i] += v[i] * inv;
+            for (int u = 0; u < 2; ++u) {
+                const int r = r0 + u * kWarps * G + grp;
+                load_logits<kF32>(p.logits, (r < stop ? r : r0) * p.ld, e0, p.E, p.vec, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = r0 + u * kWarps * G + grp;
+                const float total = scores<TPR>(v[u], p.eps);
+                if (r < stop) {
+                    // eps may be 0 and every score may have underflowed: no share then
+                    const float inv = total == 0.f ? 0.f : 1.0f / total;
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) acc[i] += v[u][i] * inv;
+                }
             }
         }
         for (int64_t i = static_cast<int64_t>(t) * p.k + threadIdx.x; i < static_cast<int64_t>(stop) * p.k;
@@ -192,9 +204,35 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(FwdParams p) 
     }
 }
 
-__global__ void __launch_bounds__(kThreads) balance_finish_kernel(FwdParams p) {
-    __shared__ double sum_s[kThreads];
-    __shared__ int cnt_s[kThreads];
+// Sums of f and n over the block in a fixed order, in thread 0.
+__device__ __forceinline__ void block_sum(double &f, int &n, double *fs, int *ns) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        f += __shfl_down_sync(0xffffffffu, f, o);
+        n += __shfl_down_sync(0xffffffffu, n, o);
+    }
+    __syncthreads();
+    if (lane == 0) {
+        fs[warp] = f;
+        ns[warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        f = fs[lane];
+        n = ns[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            f += __shfl_down_sync(0xffffffffu, f, o);
+            n += __shfl_down_sync(0xffffffffu, n, o);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FwdParams p) {
+    static_assert(kFinishThreads == 1024, "block_sum takes 32 warps");
+    __shared__ double sum_s[kFinishThreads];
+    __shared__ int cnt_s[kFinishThreads];
     __shared__ bool last;
     const int b = blockIdx.x, tid = threadIdx.x;
     pdl_trigger();
@@ -202,22 +240,34 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(FwdParams p) {
     const int t0 = seq_at(p.seq, b, p.B, p.N), t1 = seq_at(p.seq, b + 1, p.B, p.N);
     const int T = t1 - t0;
     const int c0 = T > 0 ? t0 / p.chunk : 0, c1 = T > 0 ? (t1 - 1) / p.chunk + 1 : 0;
-    double mine = 0.0;
-    // kThreads / e_pad slots at a time, each thread one expert of them
+    // kFinishThreads / e_pad slots at a time, each thread one expert of them
     int e_pad = 1;
     while (e_pad < p.E) e_pad <<= 1;
-    const int groups = kThreads / e_pad, e = tid % e_pad, g = tid / e_pad;
+    const int groups = kFinishThreads / e_pad, e = tid % e_pad, g = tid / e_pad;
     double s = 0.0;
     int n = 0;
-    if (e < p.E)
-        for (int c = c0 + g; c < c1; c += groups) {
-            const size_t slot = static_cast<size_t>(c + b) * p.E + e;
-            s += static_cast<double>(p.part[slot]);
-            n += p.part_n[slot];
+    if (e < p.E) {
+        for (int c = c0 + g; c < c1; c += 4 * groups) {  // four slots' loads at a time
+            float f[4];
+            int m[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int cu = c + u * groups;
+                const size_t slot = static_cast<size_t>(cu + b) * p.E + e;
+                f[u] = cu < c1 ? p.part[slot] : 0.f;
+                m[u] = cu < c1 ? p.part_n[slot] : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s += static_cast<double>(f[u]);
+                n += m[u];
+            }
         }
+    }
     sum_s[tid] = s;
     cnt_s[tid] = n;
     __syncthreads();
+    double mine = 0.0;
     if (g == 0 && e < p.E) {
         for (int i = 1; i < groups; ++i) {
             s += sum_s[i * e_pad + e];
@@ -228,15 +278,10 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(FwdParams p) {
         p.counts[static_cast<size_t>(b) * p.E + e] = n;
         if (T > 0) mine = static_cast<double>(p.E) * n / (static_cast<double>(p.k) * T) * prob;
     }
-    __syncthreads();
-    sum_s[tid] = mine;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (tid < o) sum_s[tid] += sum_s[tid + o];
-        __syncthreads();
-    }
+    int none = 0;
+    block_sum(mine, none, sum_s, cnt_s);
     if (tid == 0) {
-        p.seq_loss[b] = sum_s[0];
+        p.seq_loss[b] = mine;
         __threadfence();
         last = atomicAdd(p.ticket, 1) == p.B - 1;
     }
@@ -245,23 +290,14 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(FwdParams p) {
     __threadfence();
     double total = 0.0;
     int live = 0;
-    for (int i = tid; i < p.B; i += kThreads) {
+    for (int i = tid; i < p.B; i += kFinishThreads) {
         total += *reinterpret_cast<volatile double *>(p.seq_loss + i);
         live += seq_at(p.seq, i + 1, p.B, p.N) > seq_at(p.seq, i, p.B, p.N);
     }
-    sum_s[tid] = total;
-    cnt_s[tid] = live;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-        if (tid < o) {
-            sum_s[tid] += sum_s[tid + o];
-            cnt_s[tid] += cnt_s[tid + o];
-        }
-        __syncthreads();
-    }
+    block_sum(total, live, sum_s, cnt_s);
     if (tid == 0) {
-        const double sc = cnt_s[0] > 0 ? static_cast<double>(p.coef) / cnt_s[0] : 0.0;
-        *p.loss = static_cast<float>(sc * sum_s[0]);
+        const double sc = live > 0 ? static_cast<double>(p.coef) / live : 0.0;
+        *p.loss = static_cast<float>(sc * total);
         *p.scale = static_cast<float>(sc);
     }
 }
@@ -285,9 +321,15 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BwdParams p)
     float g[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) g[i] = 0.f;
+    float ahead[kV];       // the next token's logits, in flight during this one's work
+    load_logits<kF32>(p.logits, (mine < r_end ? mine : 0) * p.ld, e0, p.E, p.vec, ahead);
     for (int j = 0; j < per; ++j) {
         const int r = mine + j;
         const bool live = r < r_end;     // the shuffles below want whole warps
+        float v[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] = ahead[i];
+        load_logits<kF32>(p.logits, (j + 1 < per && r + 1 < r_end ? r + 1 : 0) * p.ld, e0, p.E, p.vec, ahead);
         if (live && (r >= stop || j == 0)) {
             inside = false;
             if (r >= first) {
@@ -308,8 +350,6 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BwdParams p)
                 stop = first;
             }
         }
-        float v[kV];
-        load_logits<kF32>(p.logits, (live ? r : 0) * p.ld, e0, p.E, p.vec, v);
         float slope[kV];
         const float total = scores<TPR>(v, p.eps, slope);
         const float inv = total == 0.f ? 0.f : 1.0f / total;
@@ -449,7 +489,7 @@ extern "C" int moe_balance_forward(const void *logits, int dtype, int64_t ld, co
     } else if (cudaMemsetAsync(p.ticket, 0, 4, s) != cudaSuccess) {
         return MOE_ERR_CUDA;
     }
-    return launch_k(balance_finish_kernel, dim3(n_seqs), dim3(kThreads), 0, s, p);
+    return launch_k(balance_finish_kernel, dim3(n_seqs), dim3(kFinishThreads), 0, s, p);
 }
 
 extern "C" int moe_balance_backward(const void *logits, int dtype, int64_t ld,
