@@ -46,8 +46,12 @@ extern "C" {
  * 128x128 block, weight = code value * block scale. Inside the forward each
  * token's input to gate/up and its SiLU(gate)*up row are quantised in groups
  * of 128 columns: s = max|v| / 448, code = e4m3(v / s) rounded to nearest
- * even with saturation (s = 0 and zero codes for an all-zero group). */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_BLOCK = 2 } moe_dtype;
+ * even with saturation (s = 0 and zero codes for an all-zero group).
+ * MOE_MXFP4 keeps the expert matrices in the 4-bit format of mx.h, one E8M0
+ * scale per 32 values of a row; x and out are bf16. Inside the forward the
+ * normalised rows and the SiLU(gate)*up rows, each rounded to bf16, are
+ * quantised by moe_mx_quantize's rule and multiplied as by moe_mx_matmul. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_BLOCK = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 typedef enum {
     MOE_OK = 0,
@@ -71,11 +75,14 @@ typedef struct {
     const float *expert_bias;  /* [E]        selection-only expert bias               */
     const void  *w_gate_up;    /* [E][2I][d] rows 0..I-1 gate, rows I..2I-1 up        */
     const void  *w_down;       /* [E][d][I]  down projection                          */
+                               /* (MOE_MXFP4: codes [E][2I][d/2] and [E][d][I/2])     */
     float        routed_scale; /* multiplies the normalised weights (1 in the page)   */
-    /* MOE_FP8_BLOCK only (ignored otherwise): fp32 scales of the 128x128 blocks,
-     * block (rb, cb) covering rows rb*128.. and columns cb*128.. of a matrix. */
-    const float *w_gate_up_scale; /* [E][2I/128][d/128]                               */
-    const float *w_down_scale;    /* [E][d/128][I/128]                                */
+    /* MOE_FP8_BLOCK: fp32 scales of the 128x128 blocks, block (rb, cb) covering
+     * rows rb*128.. and columns cb*128.. of a matrix, [E][2I/128][d/128] and
+     * [E][d/128][I/128]. MOE_MXFP4: uint8 E8M0 scales [E][2I][d/32] and
+     * [E][d][I/32]. Ignored otherwise. */
+    const void *w_gate_up_scale;
+    const void *w_down_scale;
 } moe_weights;
 
 typedef struct moe_ctx moe_ctx;
@@ -87,12 +94,14 @@ typedef struct moe_ctx moe_ctx;
  * Supported: 1 <= top_k <= min(n_experts, 8), n_experts <= 256,
  *   MOE_F32: d % 4 == 0, any d_ff >= 1;
  *   MOE_BF16: d % 64 == 0, d_ff % 64 == 0 (tensor-core tiles);
- *   MOE_FP8_BLOCK: d % 128 == 0, d_ff % 128 == 0 (whole scale blocks).
+ *   MOE_FP8_BLOCK: d % 128 == 0, d_ff % 128 == 0 (whole scale blocks);
+ *   MOE_MXFP4: d % 128 == 0, d_ff % 128 == 0 (four scales).
  * On success *out receives the context; on failure *out is set to NULL and
  * nothing stays allocated. Synchronous. The workspace holds the grouped rows,
  * the expert intermediates and outputs of max_tokens * top_k assignments;
  * MOE_FP8_BLOCK layers add an fp32 [max_tokens * top_k][d_ff] buffer for the
- * CTA-pair path (4 bytes per intermediate value; none with MOE_FP8_PAIR=0).
+ * CTA-pair path (4 bytes per intermediate value; none with MOE_FP8_PAIR=0),
+ * MOE_MXFP4 layers the quantised copies of the grouped rows and intermediates.
  * The kernels are chosen per forward from the batch size; two environment
  * variables, read here, force the choice between kernels that compute the
  * same result (for testing and tuning): MOE_TC_PAIR=0 (bf16 expert GEMMs
@@ -103,7 +112,7 @@ int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
                const moe_weights *w, int max_tokens, moe_ctx **out);
 
 /* out[N][d] = x + MoE(RMSNorm(x)) for x[N][d] (device, dtype of the weights;
- * bf16 for MOE_FP8_BLOCK).
+ * bf16 for MOE_FP8_BLOCK and MOE_MXFP4).
  * out == x (in place) is allowed; other overlap is not. Asynchronous on
  * `stream` (a cudaStream_t, NULL = legacy default stream): no host sync, no
  * allocation, a fixed sequence of kernel launches, so it can be captured in a
@@ -155,7 +164,9 @@ int moe_kernel_times(moe_ctx *h, float *ms, int n);
  * combine when the batch was small enough for the fused expert kernel (for
  * MOE_FP8_BLOCK layers: the persistent FP8 kernel); or route, dispatch,
  * gate_up, quantize, down, combine for MOE_FP8_BLOCK batches above that size
- * (the CTA-pair FP8 GEMMs, SiLU(gate)*up quantised by its own kernel). */
+ * (the CTA-pair FP8 GEMMs, SiLU(gate)*up quantised by its own kernel); or
+ * route, dispatch, quantize, gate_up, quantize_act, down, combine for
+ * MOE_MXFP4 layers. */
 const char *moe_kernel_name(moe_ctx *h, int i);
 
 /* Number of kernel launches one forward makes for n_tokens tokens. */
@@ -173,7 +184,7 @@ int moe_selftest_timeout(moe_ctx *h, int timeout_us, void *stream);
  * device memory). The page describes no such entry point; it is an interface
  * of this library only. Computes, for x[n_tokens][d] (dtype MOE_F32 or
  * MOE_BF16: the storage type of x, so MOE_BF16 for the bf16 x of an
- * MOE_FP8_BLOCK layer, whose router is unquantised; any other dtype gives
+ * MOE_FP8_BLOCK or MOE_MXFP4 layer, whose router is unquantised; any other dtype gives
  * MOE_ERR_INVALID_ARG) and the fp32 norm_gain[d], router_w[E][d], expert_bias[E], the
  * same idx[n_tokens][top_k] (int32, slot order) and w[n_tokens][top_k] (fp32)
  * as moe_forward's routing (see moe_debug_routing). All pointers are device

@@ -18,7 +18,7 @@ from typing import Dict, List, Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_FP8_BLOCK = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_BLOCK, MOE_MXFP4 = 0, 1, 2, 3
 ERRORS = {
     0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED_SHAPE",
     -3: "MOE_ERR_ALIGNMENT", -4: "MOE_ERR_TOO_MANY_TOKENS", -5: "MOE_ERR_OOM",
@@ -169,7 +169,9 @@ class MoeLayer:
     w_gate_up [E,2I,d] and w_down [E,d,I] (both f32 or bf16), on one CUDA device.
     FP8_BLOCK layers hold e4m3 (torch.float8_e4m3fn) expert matrices plus
     w_gate_up_scale [E,2I/128,d/128] and w_down_scale [E,d/128,I/128] (f32);
-    their x and out are bf16.
+    their x and out are bf16. MXFP4 layers (mx.quantize_experts makes one) hold
+    uint8 codes w_gate_up [E,2I,d/2] and w_down [E,d,I/2] and uint8 scales
+    w_gate_up_scale [E,2I,d/32] and w_down_scale [E,d,I/32]; bf16 x and out too.
     """
 
     def __init__(self, layer: Dict, top_k: int, eps: float = 1e-6,
@@ -186,8 +188,17 @@ class MoeLayer:
         elif wgu.dtype == torch.float8_e4m3fn:
             dt = MOE_FP8_BLOCK
             names += ["w_gate_up_scale", "w_down_scale"]
+        elif wgu.dtype == torch.uint8:
+            dt = MOE_MXFP4
+            d *= 2
+            names += ["w_gate_up_scale", "w_down_scale"]
+            for n, want in (("w_gate_up", (E, twoI, d // 2)), ("w_gate_up_scale", (E, twoI, d // 32)),
+                            ("w_down", (E, d, I // 2)), ("w_down_scale", (E, d, I // 32))):
+                if layer[n].dtype != torch.uint8 or tuple(layer[n].shape) != want:
+                    raise ValueError(f"{n} must be a uint8 {want} tensor")
         else:
-            raise TypeError(f"expert weights must be f32, bf16 or e4m3, got {wgu.dtype}")
+            raise TypeError(f"expert weights must be f32, bf16, e4m3 or MXFP4 codes (uint8), "
+                            f"got {wgu.dtype}")
         self._keep = {n: layer[n].contiguous() for n in names}
         for n, t in self._keep.items():
             if not t.is_cuda:
@@ -195,13 +206,14 @@ class MoeLayer:
         self.d, self.E, self.I, self.k = d, E, I, top_k
         self.dtype = wgu.dtype
         self.fp8 = dt == MOE_FP8_BLOCK
+        scaled = dt in (MOE_FP8_BLOCK, MOE_MXFP4)
         self.max_tokens = max_tokens
         k = self._keep
         self._w = MoeWeights(dt, k["norm_gain"].data_ptr(), k["router_w"].data_ptr(),
                              k["bias"].data_ptr(), k["w_gate_up"].data_ptr(),
                              k["w_down"].data_ptr(), routed_scale,
-                             k["w_gate_up_scale"].data_ptr() if self.fp8 else None,
-                             k["w_down_scale"].data_ptr() if self.fp8 else None)
+                             k["w_gate_up_scale"].data_ptr() if scaled else None,
+                             k["w_down_scale"].data_ptr() if scaled else None)
         h = ctypes.c_void_p()
         with torch.cuda.device(wgu.device):
             _check(lib().moe_create(d, E, I, top_k, eps, ctypes.byref(self._w), max_tokens,

@@ -16,6 +16,8 @@
 // (bf16 batches of at most 32 rows per expert on average fuse 3 and 4 into one
 // persistent kernel. FP8_BLOCK layers always do: their dispatch writes e4m3
 // rows with group scales and one persistent kernel runs both contractions.)
+// MXFP4 layers quantise the grouped rows after 2 and the SiLU(gate)*up rows
+// after 3, and run 3 and 4 as the MXFP4 product (mx_matmul.cu) at every size.
 //   5 combine   out = x + sum_j w_j y_j in fixed slot order
 #include <stdio.h>
 #include <stdlib.h>
@@ -26,6 +28,7 @@
 #include <vector>
 
 #include "moe_fp8.cuh"
+#include "mx.cuh"
 
 using namespace moe;
 
@@ -49,6 +52,10 @@ struct moe_ctx {
     uint8_t *xq, *aq;
     float *xs, *as;
     float *a32;          // CTA-pair path: SiLU(gate)*up in fp32 [rows_cap][I] before quantisation
+
+    // MXFP4 layers: codes and scales of the grouped rows (xm) and of act (am)
+    bool mx;
+    uint8_t *xm, *xms, *am, *ams;
 
     void *ws;  // one allocation, carved below
     void *xp, *act, *y, *x_stage, *out_stage;
@@ -84,6 +91,8 @@ static const char *kKernelNames[] = {"route", "dispatch", "gate_up", "down", "co
 static const char *kFusedKernelNames[] = {"route", "dispatch", "experts", "combine"};
 static const char *kFp8PairKernelNames[] = {"route", "dispatch", "gate_up", "quantize", "down",
                                             "combine"};
+static const char *kMxKernelNames[] = {"route", "dispatch", "quantize", "gate_up", "quantize_act",
+                                       "down", "combine"};
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -125,13 +134,15 @@ extern "C" const char *moe_strerror(int code) {
 }
 
 static int check_shapes(int d, int E, int I, int k, int dtype, int max_tokens) {
-    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_FP8_BLOCK) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_FP8_BLOCK && dtype != MOE_MXFP4)
+        return MOE_ERR_INVALID_ARG;
     if (d <= 0 || E <= 0 || I <= 0 || k <= 0 || max_tokens <= 0) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (E > kMaxExperts || k > kMaxTopK || k > E) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (d % 4 != 0 || d > 32768) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (dtype == MOE_BF16 && (d % 64 != 0 || I % 64 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (dtype == MOE_FP8_BLOCK && (d % kFp8Block != 0 || I % kFp8Block != 0))
         return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (dtype == MOE_MXFP4 && (d % kMxWord != 0 || I % kMxWord != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
     // 32-bit row indices and TMA coordinates
     if (static_cast<long long>(max_tokens) * k >= (1LL << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<long long>(E) * 2 * I >= (1LL << 30) ||
@@ -153,7 +164,7 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
     if (!aligned16(w->norm_gain) || !aligned16(w->router_w) || !aligned16(w->w_gate_up) ||
         !aligned16(w->w_down))
         return MOE_ERR_ALIGNMENT;
-    if (w->dtype == MOE_FP8_BLOCK) {
+    if (w->dtype == MOE_FP8_BLOCK || w->dtype == MOE_MXFP4) {
         if (!w->w_gate_up_scale || !w->w_down_scale) return MOE_ERR_INVALID_ARG;
         if (!aligned16(w->w_gate_up_scale) || !aligned16(w->w_down_scale)) return MOE_ERR_ALIGNMENT;
     }
@@ -170,7 +181,8 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
     h->max_tokens = max_tokens; h->device = dev; h->n_sm = prop.multiProcessorCount;
     h->eps = eps; h->scale = w->routed_scale; h->w = *w;
     h->fp8 = (w->dtype == MOE_FP8_BLOCK);
-    h->xdtype = h->fp8 ? MOE_BF16 : w->dtype;
+    h->mx = (w->dtype == MOE_MXFP4);
+    h->xdtype = h->fp8 || h->mx ? MOE_BF16 : w->dtype;
     h->elem = (h->xdtype == MOE_F32) ? 4 : 2;
     h->use_tc = (w->dtype == MOE_BF16);
     h->rows_cap = max_tokens * top_k;
@@ -187,7 +199,7 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
         e = getenv("MOE_FP8_PAIR");
         h->fp8_pair_mode = (e && e[0] == '0') ? 0 : -1;
     }
-    h->route_tc = (h->use_tc || h->fp8) && route_tc_ok(d, n_experts);
+    h->route_tc = (h->use_tc || h->fp8 || h->mx) && route_tc_ok(d, n_experts);
 
     h->e_pad = (n_experts + 63) / 64 * 64;
     h->max_chunks = max_dispatch_chunks(n_experts);
@@ -215,9 +227,13 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
         256,                                  // status
         3 * E * static_cast<size_t>(d) * 2,   // router_w3
         (h->fp8 && h->fp8_pair_mode != 0) ? R * d_ff * 4 : 0,  // a32
+        h->mx ? R * (d / 2) : 0,                               // xm
+        h->mx ? R * (d / kMxBlock) : 0,                        // xms
+        h->mx ? R * (d_ff / 2) : 0,                            // am
+        h->mx ? R * (d_ff / kMxBlock) : 0,                     // ams
     };
-    const int nblocks = sizeof(sizes) / sizeof(sizes[0]);
-    size_t total = 0, off[20];
+    constexpr int nblocks = sizeof(sizes) / sizeof(sizes[0]);
+    size_t total = 0, off[nblocks];
     for (int i = 0; i < nblocks; ++i) {
         off[i] = total;
         total += (sizes[i] + 255) & ~static_cast<size_t>(255);
@@ -246,6 +262,7 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
     h->status = reinterpret_cast<int *>(b + off[17]);
     h->router_w3 = b + off[18];
     h->a32 = reinterpret_cast<float *>(b + off[19]);
+    h->xm = b + off[20]; h->xms = b + off[21]; h->am = b + off[22]; h->ams = b + off[23];
     if (h->fp8) {  // codes then scales, inside the (2-byte element) xp and act blocks
         h->xq = static_cast<uint8_t *>(h->xp);
         h->xs = reinterpret_cast<float *>(h->xq + R * d);
@@ -293,6 +310,15 @@ extern "C" int moe_create(int d, int n_experts, int d_ff, int top_k, float eps,
         if (rc != MOE_OK) {
             if (h->fp8_maps) fp8_free_maps(h->fp8_maps);
             if (h->fp8_pair_maps) fp8_pair_free_maps(h->fp8_pair_maps);
+            cudaFree(h->ws);
+            delete h;
+            return rc;
+        }
+    }
+    if (h->mx && h->route_tc) {
+        rc = tc_encode_2d(&h->w3_map, h->router_w3, 3 * static_cast<uint64_t>(n_experts), d,
+                          3 * n_experts);
+        if (rc != MOE_OK) {
             cudaFree(h->ws);
             delete h;
             return rc;
@@ -431,7 +457,8 @@ static int forward_impl(moe_ctx *h, const void *x, void *out, int N, cudaStream_
     if (fp8_pair) {
         Fp8PairParams fp;
         fp.offsets = h->offsets; fp.mt_start = h->mt_start;
-        fp.sgu = h->w.w_gate_up_scale; fp.sdn = h->w.w_down_scale;
+        fp.sgu = static_cast<const float *>(h->w.w_gate_up_scale);
+        fp.sdn = static_cast<const float *>(h->w.w_down_scale);
         fp.xs = h->xs; fp.as_in = h->as; fp.a32 = h->a32; fp.aq = h->aq; fp.as_out = h->as;
         fp.y = h->y; fp.status = h->status; fp.E = h->E; fp.d = h->d; fp.I = h->I;
         MOE_TRY(launch_fp8_pair_gate_up(h->fp8_pair_maps, fp, h->n_sm, s));
@@ -442,13 +469,35 @@ static int forward_impl(moe_ctx *h, const void *x, void *out, int N, cudaStream_
         MOE_MARK();
     } else if (h->fp8) {
         Fp8ExpertParams fp;
-        fp.offsets = h->offsets; fp.sgu = h->w.w_gate_up_scale; fp.sdn = h->w.w_down_scale;
+        fp.offsets = h->offsets; fp.sgu = static_cast<const float *>(h->w.w_gate_up_scale);
+        fp.sdn = static_cast<const float *>(h->w.w_down_scale);
         fp.xs = h->xs; fp.aq = h->aq; fp.as = h->as; fp.y = h->y; fp.sched = h->sched;
         fp.status = h->status; fp.E = h->E; fp.d = h->d; fp.I = h->I;
         // passes of 32 tokens (more TMEM buffers) while the mean load is small
         const bool small = static_cast<long long>(N) * h->k <=
                            static_cast<long long>(kDecodeRowsPerExpert) * h->E;
         MOE_TRY(launch_fp8_experts(h->fp8_maps, fp, h->n_sm, small ? 32 : 64, s));
+        MOE_MARK();
+    } else if (h->mx) {
+        const int rows = N * h->k;
+        MxMatmulParams mp = {};
+        mp.offsets = h->offsets; mp.status = h->status; mp.rows = rows; mp.E = h->E;
+        mp.dtype = MOE_BF16;
+        MOE_TRY(launch_mx_quantize(h->xp, MOE_BF16, rows, h->d, h->d, h->xm, h->xms, s));
+        MOE_MARK();
+        mp.a = h->xm; mp.as = h->xms;
+        mp.w = static_cast<const uint8_t *>(h->w.w_gate_up);
+        mp.ws = static_cast<const uint8_t *>(h->w.w_gate_up_scale);
+        mp.K = h->d; mp.N = 2 * h->I; mp.silu_mul = 1; mp.out = h->act;
+        MOE_TRY(launch_mx_matmul(mp, h->n_sm, s));
+        MOE_MARK();
+        MOE_TRY(launch_mx_quantize(h->act, MOE_BF16, rows, h->I, h->I, h->am, h->ams, s));
+        MOE_MARK();
+        mp.a = h->am; mp.as = h->ams;
+        mp.w = static_cast<const uint8_t *>(h->w.w_down);
+        mp.ws = static_cast<const uint8_t *>(h->w.w_down_scale);
+        mp.K = h->I; mp.N = h->d; mp.silu_mul = 0; mp.out = h->y;
+        MOE_TRY(launch_mx_matmul(mp, h->n_sm, s));
         MOE_MARK();
     } else if (fused) {
         DecodeParams fp;
@@ -627,6 +676,7 @@ extern "C" int moe_kernel_times(moe_ctx *h, float *ms, int n) {
 
 extern "C" const char *moe_kernel_name(moe_ctx *h, int i) {
     if (!h) return nullptr;
+    if (h->mx) return (i >= 0 && i < 7) ? kMxKernelNames[i] : nullptr;
     if (h->last_fused) return (i >= 0 && i < 4) ? kFusedKernelNames[i] : nullptr;
     if (h->last_fp8_pair) return (i >= 0 && i < 6) ? kFp8PairKernelNames[i] : nullptr;
     return (i >= 0 && i < 5) ? kKernelNames[i] : nullptr;
@@ -635,6 +685,7 @@ extern "C" const char *moe_kernel_name(moe_ctx *h, int i) {
 extern "C" int moe_launches_per_forward(moe_ctx *h, int n_tokens) {
     if (!h) return MOE_ERR_INVALID_ARG;
     if (n_tokens <= 0) return 0;
+    if (h->mx) return 7;
     return use_fused_experts(h, n_tokens) ? 4 : use_fp8_pair(h, n_tokens) ? 6 : 5;
 }
 

@@ -193,6 +193,18 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
     return out
 
 
+def quantize_experts(layer):
+    """A MoeLayer dict with its expert matrices (f32 or bf16) in MXFP4: codes under
+    w_gate_up and w_down, scales under w_gate_up_scale and w_down_scale; the rest
+    as it was. Widths must be multiples of 128."""
+    out = dict(layer)
+    for name in ("w_gate_up", "w_down"):
+        if layer[name].shape[-1] % 128:
+            raise ValueError(f"{name}: rows of a multiple of 128 values")
+        out[name], out[name + "_scale"] = quantize(layer[name])
+    return out
+
+
 def status(device=None) -> int:
     """Waits for the device; 0, or the code of a time-out inside a matmul on it
     since the last call (whose result is then incomplete)."""

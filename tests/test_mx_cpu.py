@@ -84,3 +84,28 @@ def test_reference_rounding():
     assert R.quantize(np.full((1, 32), 2.0 ** -149))[1][0, 0] == 0
     z, s = R.quantize(np.zeros((1, 32)))
     assert s[0, 0] == 0 and not z.any()
+
+
+def test_mxfp4_layer_refusals():
+    """moe_create checks an MXFP4 layer's shapes, scale arrays and alignment
+    before any device work; expert-parallel contexts do not take one."""
+    import ctypes
+
+    import sigmoid_bias_top_b200 as sb
+    L = sb.lib()
+
+    def create(d=2048, I=1536, scales=(256, 256)):
+        h = ctypes.c_void_p(7)
+        w = sb.MoeWeights(sb.MOE_MXFP4, 256, 256, 256, 256, 256, 1.0, *scales)
+        rc = L.moe_create(d, 64, I, 4, 1e-6, ctypes.byref(w), 16, ctypes.byref(h))
+        assert not h.value or rc == 0
+        return rc
+    assert create(d=2112) == -2 and create(I=1600) == -2
+    assert create(scales=(None, 256)) == -1 and create(scales=(256, None)) == -1
+    assert create(scales=(256, 264)) == -3
+    h = ctypes.c_void_p(7)
+    w = sb.MoeWeights(sb.MOE_MXFP4, 256, 256, 256, 256, 256, 1.0, 256, 256)
+    assert L.moe_ep_create(2048, 64, 1536, 4, 1e-6, ctypes.byref(w), 16, 0, 8, 64,
+                           ctypes.byref(h)) == -1
+    assert L.moe_route_noalloc(256, sb.MOE_MXFP4, 256, 256, 256, 8, 256, 16, 4, 1e-6, 1.0, 256, 256,
+                               None) == -1
