@@ -35,6 +35,7 @@
 // All waits are bounded (1 s) and report a time-out in the status word; the
 // kernel then drains its copies and MMAs, frees TMEM and returns.
 #include <cooperative_groups.h>
+#include <stddef.h>
 
 #include "mx.cuh"
 
@@ -75,11 +76,14 @@ struct Cfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
     static constexpr int STAGES = kPair ? 3 : 4;
     static constexpr int SF_COLS = KWORDS * (4 + 4 * NB);  // TMEM columns of a stage's scales
-    static constexpr int SF_SLOTS = 2;                     // sets of them
+    static constexpr int SF_SLOTS = kPair ? 2 : 4;         // sets of them
     static constexpr int USED_COLS = 2 * NT + SF_SLOTS * SF_COLS;
     static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
-    static constexpr int N_STEP = kPair ? 32 : 16;     // the MMA's N is a multiple of it
+    static constexpr int N_STEP = 16;                  // the MMA's N is a multiple of it
     static_assert(USED_COLS <= 512 && STAGES <= kMaxStages, "TMEM");
+    // a slot's last MMAs are waited for on their stage's barrier, which a later
+    // stage must not have gone through again by then
+    static_assert(SF_SLOTS <= STAGES, "slots");
     static_assert(B_SUB % 1024 == 0 && SF_BYTES % 1024 == 0, "swizzle atoms");
 };
 
@@ -96,16 +100,62 @@ struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
     int abort;
 };
 
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Ctl *ctl, int *status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (mbar_wait(bar, parity, globaltimer_ns() + kWaitNs)) return true;
+// Barriers by their shared addresses (one register, no conversion from generic
+// pointers: the roles' loops are bound by their instructions' latencies).
+__device__ __forceinline__ bool try_bar(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool aborted(Ctl *ctl) {
+    return *reinterpret_cast<volatile int *>(&ctl->abort) != 0;
+}
+
+__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, Ctl *ctl, int *status) {
+    const uint64_t deadline = globaltimer_ns() + kWaitNs;
+    for (uint32_t i = 0;; ++i) {
+        if (try_bar(bar, parity)) return true;
+        if ((i & 255u) == 255u) {
+            if (aborted(ctl)) return false;
+            if (globaltimer_ns() > deadline) break;
+        }
+    }
     set_status(status, kStatusTimeout);
     atomicExch(&ctl->abort, 1);
     return false;
 }
 
-__device__ __forceinline__ bool aborted(Ctl *ctl) {
-    return *reinterpret_cast<volatile int *>(&ctl->abort) != 0;
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl *ctl, int *status) {
+    // a try suspends the thread for a while by itself; a few of them cover any
+    // wait of a running pipeline
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (try_bar(bar, parity)) return true;
+    return wait_bar_slow(bar, parity, ctl, status);
+}
+
+__device__ __forceinline__ void arrive_bar(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void arrive_bar_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 // True in one lane of the (converged) warp. The compiler knows that a region
@@ -127,9 +177,9 @@ __device__ __forceinline__ bool elect_one() {
 // thread's TMEM accesses, which the caller has fenced, and nothing else: a
 // release to the cluster would wait for all of the thread's global accesses in
 // flight (over 700 cycles a stage).
-__device__ __forceinline__ void mbar_arrive_leader(uint64_t *bar) {
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
     uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
@@ -163,33 +213,37 @@ struct Tc {
         else
             tmem_dealloc(taddr, cols);
     }
-    static __device__ __forceinline__ void load_2d(void *dst, const CUtensorMap *m, int x, int y,
-                                                   uint64_t *bar) {
+    // dst and bar are shared addresses
+    static __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *m, int x, int y,
+                                                   uint32_t bar) {
         if constexpr (kPair)
             asm volatile(
                 "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar) & kPeerBitMask)
+                " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar & kPeerBitMask)
                 : "memory");
         else
-            tma_load_2d(dst, m, x, y, bar);
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+                : "memory");
     }
-    // Box {64 two-byte columns, 16 rows, gate|up, 4 row groups} of the paired-row view.
-    static __device__ __forceinline__ void load_4d(void *dst, const CUtensorMap *m, int x, int group,
-                                                   uint64_t *bar) {
+    // Box {two-byte columns, 16 rows, gate|up, 4 row groups} of the paired-row view.
+    static __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap *m, int x, int group,
+                                                   uint32_t bar) {
         if constexpr (kPair)
             asm volatile(
                 "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
                 "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group),
-                "r"(smem_u32(bar) & kPeerBitMask)
+                "r"(bar & kPeerBitMask)
                 : "memory");
         else
             asm volatile(
                 "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group),
-                "r"(smem_u32(bar))
+                " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+                "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(0), "r"(0), "r"(group), "r"(bar)
                 : "memory");
     }
     // a, b: low words of the operands' descriptors (kDescHigh: the high word of both)
@@ -217,24 +271,24 @@ struct Tc {
                 : "memory");
     }
     // one arrival on `bar`, in both CTAs of a pair, when this thread's tcgen05 work is done
-    static __device__ __forceinline__ void commit(uint64_t *bar) {
+    static __device__ __forceinline__ void commit(uint32_t bar) {
         if constexpr (kPair)
             asm volatile(
                 "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
                 "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                " [%0], m;\n\t}" ::"r"(smem_u32(bar))
+                " [%0], m;\n\t}" ::"r"(bar)
                 : "memory");
         else
-            umma_commit(bar);
+            commit_here(bar);
     }
     // the same on this CTA's barrier alone
-    static __device__ __forceinline__ void commit_here(uint64_t *bar) {
+    static __device__ __forceinline__ void commit_here(uint32_t bar) {
         if constexpr (kPair)
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                             smem_u32(bar))
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                          : "memory");
         else
-            umma_commit(bar);
+            asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                         : "memory");
     }
 };
 
@@ -280,31 +334,36 @@ __device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts, con
     return it;
 }
 
-// A role's walk along the dealt items. kWarp: the whole warp walks together.
+// The shared addresses of a barrier of Ctl, at base `bars` (that of the Ctl).
+#define MX_BAR(field, i) (bars + static_cast<uint32_t>(offsetof(Ctl, field)) + 8u * static_cast<uint32_t>(i))
+
+// A role's walk along the dealt items, which follow the Ctl. kWarp: the whole
+// warp walks together.
 template <bool kWarp>
 struct Walk {
     Ctl *ctl;
-    const Item *items;  // [2][kDeal]
     int *status;
+    uint32_t bars;
     int i;
 
-    __device__ __forceinline__ Walk(Ctl *c, const Item *it, int *st)
-        : ctl(c), items(it), status(st), i(0) {}
+    __device__ __forceinline__ Walk(Ctl *c, uint32_t b, int *st) : ctl(c), status(st), bars(b), i(0) {}
 
     // false at the end of the list, or after a time-out
     __device__ __forceinline__ bool next(Item &it) {
         const int set = (i / kDeal) & 1;
-        if (i % kDeal == 0 &&
-            !wait_bar(&ctl->dealt[set], (i / (2 * kDeal)) & 1u, ctl, status))
-            return false;
-        const int4 v = *reinterpret_cast<const int4 *>(items + set * kDeal + i % kDeal);
-        it.wrow = v.x; it.wt = v.y; it.t0 = v.z; it.rows = v.w;
+        if (i % kDeal == 0 && !wait_bar(MX_BAR(dealt, set), (i / (2 * kDeal)) & 1u, ctl, status)) return false;
+        const uint4 v = ld_shared(bars + static_cast<uint32_t>(sizeof(Ctl)) +
+                                  (set * kDeal + i % kDeal) * static_cast<uint32_t>(sizeof(Item)));
+        it.wrow = static_cast<int>(v.x);
+        it.wt = static_cast<int>(v.y);
+        it.t0 = static_cast<int>(v.z);
+        it.rows = static_cast<int>(v.w);
         if (i % kDeal == kDeal - 1) {
             if (kWarp) __syncwarp();
-            if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ctl->taken[set]);
+            if (!kWarp || (threadIdx.x & 31) == 0) arrive_bar(MX_BAR(taken, set));
         }
         ++i;
-        return it.rows > 0 && !aborted(ctl);
+        return it.rows > 0;
     }
 };
 
@@ -353,28 +412,28 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *src, size_t row, int 
 // the tile's) and of the tile's rows, stage by stage, to its TMEM quarter. Rows
 // past the tile's end have any scales; their products are never stored.
 template <typename C, bool kPair, bool kSilu>
-__device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, const Item *items,
-                                             const uint8_t *smem, uint32_t tmem_sf, int NO, int o_base,
+__device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, uint32_t bars,
+                                             uint32_t smem, uint32_t tmem_sf, int NO, int o_base,
                                              int tile_outputs, int nk) {
     static_assert(KWORDS == 4, "a row's 16 bytes are a stage");
     const int lane = threadIdx.x & 31;
     const uint32_t taddr = tmem_sf + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
-    Walk<true> walk(ctl, items, p.status);
+    Walk<true> walk(ctl, bars, p.status);
     Item it;
-    int s = 0, g = 0;  // stage of the ring, and counted from the first
-    uint32_t ph = 0;
+    int s = 0, slot = 0;       // of the rings of stages and of TMEM columns
+    int os = 0, warmup = C::SF_SLOTS;  // the stage that used the slot before, if one did
+    uint32_t ph = 0, oph = 0;
     while (walk.next(it)) {
         const int o_last = NO - 1 - it.wt * tile_outputs;
         for (int kb = 0; kb < nk; ++kb) {
             uint4 a[4], b[4 * C::NB];
             if (p.sf_tma) {
-                if (!wait_bar(&ctl->scaled[s], ph, ctl, p.status)) return;
-                const uint8_t *sf = smem + s * C::STAGE_BYTES + A_BYTES + C::B_BYTES + lane * 16;
+                if (!wait_bar(MX_BAR(scaled, s), ph, ctl, p.status)) return;
+                const uint32_t sf = smem + s * C::STAGE_BYTES + A_BYTES + C::B_BYTES + lane * 16;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const uint4 *>(sf + i * 512);
+                for (int i = 0; i < 4; ++i) a[i] = ld_shared(sf + i * 512);
 #pragma unroll
-                for (int i = 0; i < 4 * C::NB; ++i)
-                    b[i] = i < C::R ? *reinterpret_cast<const uint4 *>(sf + WM * 16 + i * 512) : b[0];
+                for (int i = 0; i < 4 * C::NB; ++i) b[i] = i < C::R ? ld_shared(sf + WM * 16 + i * 512) : b[0];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -390,22 +449,24 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
                                     : b[0];
             }
             // the MMAs that read the slot's last scales are done
-            const int o = g - C::SF_SLOTS;
-            if (o >= 0 && !wait_bar(&ctl->empty[o % C::STAGES], static_cast<uint32_t>(o / C::STAGES) & 1u,
-                                    ctl, p.status))
-                return;
+            if (warmup > 0) {
+                --warmup;
+            } else {
+                if (!wait_bar(MX_BAR(empty, os), oph, ctl, p.status)) return;
+                if (++os == C::STAGES) { os = 0; oph ^= 1u; }
+            }
             tc_fence_after();
-            const uint32_t to = taddr + static_cast<uint32_t>((g % C::SF_SLOTS) * C::SF_COLS);
+            const uint32_t to = taddr + static_cast<uint32_t>(slot * C::SF_COLS);
+            if (++slot == C::SF_SLOTS) slot = 0;
             store_words(to, a);
             store_words(to + 4 * KWORDS, b);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (kPair) mbar_arrive_leader(&ctl->full[s]);
-                else mbar_arrive(&ctl->full[s]);
+                if constexpr (kPair) arrive_leader(MX_BAR(full, s));
+                else arrive_bar(MX_BAR(full, s));
             }
-            ++g;
             if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
     }
@@ -491,10 +552,7 @@ struct Drain {
             uint4 v[kPieces];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                             : "r"(stage + (i * 32 + lane) / kPieces * kPitch + (lane % kPieces) * 16)
-                             : "memory");
+                v[i] = ld_shared(stage + (i * 32 + lane) / kPieces * kPitch + (lane % kPieces) * 16);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int r = (i * 32 + lane) / kPieces;
@@ -538,6 +596,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     Item *items = reinterpret_cast<Item *>(ctl + 1);       // [2][kDeal]
     int32_t *mts = reinterpret_cast<int32_t *>(items + 2 * kDeal);  // [E+1] prefix of row tiles
     int32_t *offs = mts + (p.E + 1);                        // [E+1]
+    const uint32_t base = smem_u32(smem), bars = smem_u32(ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.E;
     const int half = kPair ? static_cast<int>(blockIdx.x & 1) : 0;  // rank in the cluster of two
@@ -619,30 +678,30 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             uint32_t issued_parity[C::STAGES];
             for (int i = 0; i < C::STAGES; ++i) issued[i] = false;
             bool ok = true;
-            Walk<false> walk(ctl, items, p.status);
+            Walk<false> walk(ctl, bars, p.status);
             Item it;
             while (ok && walk.next(it)) {
                 const int wrow = it.wrow + half * kCtaOutputs;
                 const int trow = it.t0 + half * (mma_n<C>(it) / 2);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(&ctl->empty[s], ph ^ 1u, ctl, p.status)) { ok = false; break; }
-                    uint8_t *sa = smem + s * C::STAGE_BYTES;
-                    if (leader) mbar_arrive_expect_tx(&ctl->full[s], kCtas * (weights ? A_BYTES : C::B_BYTES));
+                    if (!wait_bar(MX_BAR(empty, s), ph ^ 1u, ctl, p.status)) { ok = false; break; }
+                    const uint32_t sa = base + s * C::STAGE_BYTES, full = MX_BAR(full, s);
+                    if (leader) arrive_bar_tx(full, kCtas * (weights ? A_BYTES : C::B_BYTES));
                     // the maps count two-byte columns: 64 of them are a box; what lies
                     // past K arrives as zeros
 #pragma unroll
                     for (int j = 0; j < KSUB; ++j) {
                         const int x = (kb * KSUB + j) * 64;
-                        if (!weights) X::load_2d(sa + A_BYTES + j * C::B_SUB, &tmA, x, trow, &ctl->full[s]);
-                        else if (kSilu) X::load_4d(sa + j * A_SUB, &tmW, x, wrow / 16, &ctl->full[s]);
-                        else X::load_2d(sa + j * A_SUB, &tmW, x, wrow, &ctl->full[s]);
+                        if (!weights) X::load_2d(sa + A_BYTES + j * C::B_SUB, &tmA, x, trow, full);
+                        else if (kSilu) X::load_4d(sa + j * A_SUB, &tmW, x, wrow / 16, full);
+                        else X::load_2d(sa + j * A_SUB, &tmW, x, wrow, full);
                     }
                     if (p.sf_tma) {  // every CTA its own weight rows' scales and all of the tile's rows'
-                        uint8_t *sf = sa + A_BYTES + C::B_BYTES;
-                        mbar_arrive_expect_tx(&ctl->scaled[s], (weights ? WM : NT) * 16);
-                        if (!weights) tma_load_2d(sf + WM * 16, &tmSA, kb * 8, it.t0, &ctl->scaled[s]);
-                        else if (kSilu) Tc<false>::load_4d(sf, &tmSW, kb * 8, wrow / 16, &ctl->scaled[s]);
-                        else tma_load_2d(sf, &tmSW, kb * 8, wrow, &ctl->scaled[s]);
+                        const uint32_t sf = sa + A_BYTES + C::B_BYTES, scaled = MX_BAR(scaled, s);
+                        arrive_bar_tx(scaled, (weights ? WM : NT) * 16);
+                        if (!weights) Tc<false>::load_2d(sf + WM * 16, &tmSA, kb * 8, it.t0, scaled);
+                        else if (kSilu) Tc<false>::load_4d(sf, &tmSW, kb * 8, wrow / 16, scaled);
+                        else Tc<false>::load_2d(sf, &tmSW, kb * 8, wrow, scaled);
                     }
                     issued[s] = true;
                     issued_parity[s] = ph;
@@ -663,23 +722,23 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     } else if (warp == 1) {
         if (leader && elect_one()) {
             // ----------------------------- MMA ------------------------------
-            const uint32_t desc0 = desc_low(smem_u32(smem));
+            const uint32_t desc0 = desc_low(base);
             int s = 0, tile = 0, slot = 0;
             uint32_t ph = 0;
             bool any = false;
-            Walk<false> walk(ctl, items, p.status);
+            Walk<false> walk(ctl, bars, p.status);
             Item it;
             for (; walk.next(it); ++tile) {
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
-                if (!wait_bar(&ctl->tempty[buf], (use & 1u) ^ 1u, ctl, p.status)) break;
+                if (!wait_bar(MX_BAR(tempty, buf), (use & 1u) ^ 1u, ctl, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * NT);
                 const int n = mma_n<C>(it);
                 const uint32_t idesc[2] = {idesc_mxf4(kCtas * WM, n, 0), idesc_mxf4(kCtas * WM, n, 1)};
                 bool ok = true;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(&ctl->full[s], ph, ctl, p.status)) { ok = false; break; }
+                    if (!wait_bar(MX_BAR(full, s), ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a0 = desc0 + static_cast<uint32_t>(s) * (C::STAGE_BYTES / 16);
                     const uint32_t b0 = a0 + A_BYTES / 16;
@@ -692,24 +751,24 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                                ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
                     if (++slot == C::SF_SLOTS) slot = 0;
                     any = true;
-                    X::commit(&ctl->empty[s]);
+                    X::commit(MX_BAR(empty, s));
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
-                X::commit(&ctl->tfull[buf]);
+                X::commit(MX_BAR(tfull, buf));
             }
             if (any) {
-                X::commit_here(&ctl->drain);
+                X::commit_here(MX_BAR(drain, 0));
                 mbar_wait(&ctl->drain, 0, globaltimer_ns() + kWaitNs);
             }
         }
     } else if (warp < 2 + kScaleWarps) {
         // ---------------------------- scales ----------------------------
-        bring_scales<C, kPair, kSilu>(p, ctl, items, smem, tmem_sf, NO, half * kCtaOutputs, kOutputs, nk);
+        bring_scales<C, kPair, kSilu>(p, ctl, bars, base, tmem_sf, NO, half * kCtaOutputs, kOutputs, nk);
     } else if (warp == kThreads / 32 - 2) {
         // ------------------------- item dealer --------------------------
         for (int c = 0;; ++c) {
-            if (c >= 2 && !wait_bar(&ctl->taken[c & 1], ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
+            if (c >= 2 && !wait_bar(MX_BAR(taken, c & 1), ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
             const int64_t item = blockIdx.x / kCtas +
                                  (static_cast<int64_t>(c) * kDeal + lane) * (gridDim.x / kCtas);
             Item it = {0, 0, 0, 0};
@@ -717,7 +776,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 it = decode(static_cast<int>(item), NW, mts, offs, E, p.N, kOutputs, C::N_STEP);
             items[(c & 1) * kDeal + lane] = it;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->dealt[c & 1]);
+            if (lane == 0) arrive_bar(MX_BAR(dealt, c & 1));
             if (__any_sync(0xffffffffu, it.rows == 0) || aborted(ctl)) break;
         }
     } else {
@@ -728,12 +787,12 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
         const uint32_t stage = smem_u32(stages_out) + ew * Drain<kSilu, T>::kStage;
         T *out = static_cast<T *>(p.out);
         int tile = 0;
-        Walk<true> walk(ctl, items, p.status);
+        Walk<true> walk(ctl, bars, p.status);
         Item it;
         for (; walk.next(it); ++tile) {
             const int buf = tile & 1;
             const uint32_t use = static_cast<uint32_t>(tile >> 1);
-            if (!wait_bar(&ctl->tfull[buf], use & 1u, ctl, p.status)) break;
+            if (!wait_bar(MX_BAR(tfull, buf), use & 1u, ctl, p.status)) break;
             tc_fence_after();
             const uint32_t t_lane = tmem_base + static_cast<uint32_t>(buf * NT) +
                                     (static_cast<uint32_t>(q * 32) << 16);
@@ -745,8 +804,8 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (kPair) mbar_arrive_leader(&ctl->tempty[buf]);
-                else mbar_arrive(&ctl->tempty[buf]);
+                if constexpr (kPair) arrive_leader(MX_BAR(tempty, buf));
+                else arrive_bar(MX_BAR(tempty, buf));
             }
         }
     }
