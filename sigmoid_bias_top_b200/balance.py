@@ -63,10 +63,10 @@ class _BalanceLoss(torch.autograd.Function):
         k, dev = idx.shape[1], logits.device
         B = 1 if seq_offsets is None else seq_offsets.numel() - 1
         L = lib()
-        both = torch.empty(2, dtype=torch.float32, device=dev)   # loss, scale
-        counts = torch.empty(B, E, dtype=torch.int32, device=dev)
-        prob = torch.empty(B, E, dtype=torch.float32, device=dev)
-        ws = torch.empty(L.moe_balance_workspace(n, E, B), dtype=torch.uint8, device=dev)
+        both = logits.new_empty(2, dtype=torch.float32)   # loss, scale
+        counts = idx.new_empty((B, E))
+        prob = logits.new_empty((B, E), dtype=torch.float32)
+        ws = idx.new_empty((L.moe_balance_workspace(n, E, B) + 3) // 4)
         ptr = both.data_ptr()
         _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
                                      idx.data_ptr(), _ptr(seq_offsets), n, E, k, B, coef, eps,
@@ -86,7 +86,7 @@ class _BalanceLoss(torch.autograd.Function):
         logits, counts, both, seq_offsets = ctx.saved_tensors
         n, E = logits.shape
         dev = logits.device
-        grad = torch.empty(n, E, dtype=logits.dtype, device=dev)
+        grad = logits.new_empty((n, E))
         # autograd runs this with the forward call's device and stream current
         _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
                                           counts.data_ptr(), _ptr(seq_offsets),

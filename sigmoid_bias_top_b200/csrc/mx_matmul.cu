@@ -944,8 +944,19 @@ int status_address(int **out) {
 
 }  // namespace
 
+// The tile by the mean rows per expert (the counts themselves are on the
+// device). Few rows are bound by the weights' stream: one CTA per 128 weight
+// rows, tiles of 32 rows up to 16 per expert (64 experts, K 2048, I 1536: 38.8 us
+// at 4 rows each, 39.4 in tiles of 48) and of 48 up to 48 (uneven loads of 32 on
+// average: 27.1 us, 28.9 in tiles of 32; even ones of 64: 48.4, pairs 44.0).
+// Above, pairs of CTAs with tiles of 192, unless the pairs' tiles would occupy
+// less than two thirds of the GPU (one matrix, K 2048, N 6144: 256 rows 8.4 us in
+// tiles of 48, 9.5 on pairs; 512 rows 9.2 us on pairs, 14.8 in tiles of 32).
 int launch_mx_matmul(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
-    return p.rows <= 32 * p.E ? launch_nt<32, false>(p, n_sm, s) : launch_nt<192, true>(p, n_sm, s);
+    const int64_t pair_tiles = static_cast<int64_t>(p.rows / 192 + p.E) * ((p.N + 2 * WM - 1) / (2 * WM));
+    if (p.rows <= 16 * p.E) return launch_nt<32, false>(p, n_sm, s);
+    if (p.rows <= 48 * p.E || 3 * pair_tiles <= n_sm) return launch_nt<48, false>(p, n_sm, s);
+    return launch_nt<192, true>(p, n_sm, s);
 }
 
 }  // namespace moe

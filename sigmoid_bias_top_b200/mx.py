@@ -96,8 +96,7 @@ def _mx(name: str, q: MxTensor, least: int, most: int):
 
 
 def _out(out: Optional[torch.Tensor], shape, dtype, device):
-    if out is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
+    """Checks an output that the caller gave."""
     if (out.dtype != dtype or tuple(out.shape) != tuple(shape) or out.device != device
             or not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous {dtype} {tuple(shape)} tensor on {device}")
@@ -129,9 +128,12 @@ def quantize(x: torch.Tensor, out: Optional[MxTensor] = None, stream=None) -> Mx
         x, ld = x.clone(memory_format=torch.contiguous_format), K
         ptr = x.data_ptr()
     lead = shape[:-1]
-    given = (None, None) if out is None else out
-    codes = _out(given[0], (*lead, K // 2), torch.uint8, device)
-    scales = _out(given[1], (*lead, K // BLOCK), torch.uint8, device)
+    if out is None:
+        codes = x.new_empty((*lead, K // 2), dtype=torch.uint8)
+        scales = x.new_empty((*lead, K // BLOCK), dtype=torch.uint8)
+    else:
+        codes = _out(out[0], (*lead, K // 2), torch.uint8, device)
+        scales = _out(out[1], (*lead, K // BLOCK), torch.uint8, device)
     _check(lib().moe_mx_quantize(ptr, dt, x.numel() // K, K, ld, codes.data_ptr(),
                                  scales.data_ptr(), _raw_stream(device.index)), "moe_mx_quantize")
     return MxTensor(codes, scales)
@@ -150,7 +152,10 @@ def dequantize(q: MxTensor, dtype=torch.bfloat16, out=None, stream=None) -> torc
     if not _here(device, stream):
         with _On(device, stream):
             return dequantize(q, dtype, out)
-    out = _out(out, (*shape[:-1], K), dtype, device)
+    if out is None:
+        out = codes.new_empty((*shape[:-1], K), dtype=dtype)
+    else:
+        _out(out, (*shape[:-1], K), dtype, device)
     _check(lib().moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.numel() // K, K,
                                    out.data_ptr(), dt, _raw_stream(device.index)),
            "moe_mx_dequantize")
@@ -186,7 +191,10 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
     if not _here(device, stream):
         with _On(device, stream):
             return matmul(a, w, offsets, silu_mul, dtype, out)
-    out = _out(out, (rows, N // 2 if silu_mul else N), dtype, device)
+    if out is None:
+        out = ac.new_empty((rows, N // 2 if silu_mul else N), dtype=dtype)
+    else:
+        _out(out, (rows, N // 2 if silu_mul else N), dtype, device)
     _check(lib().moe_mx_matmul(ac.data_ptr(), as_.data_ptr(), wc.data_ptr(), ws.data_ptr(), offs,
                                rows, 2 * half, E, N, 1 if silu_mul else 0, out.data_ptr(), dt,
                                _raw_stream(device.index)), "moe_mx_matmul")

@@ -167,6 +167,69 @@ def test_grouped(name, silu):
     assert torch.equal(out, again)
 
 
+# Large enough for tiles on CTA pairs (over 48 rows per expert, and tiles for most
+# of the GPU).
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,N", [(1500, 512, 2304), (1003, 640, 2976), (577, 128, 6176),
+                                      (193, 1024, 6304)])
+def test_dense_on_pairs(rows, K, N, dtype, silu):
+    a, w = make(rows, K, N, 0, rows + K + N, 1.0)
+    check_matmul(mx.matmul(a, w, silu_mul=silu, dtype=DT[dtype]), a, w, None, silu)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("K", [384, 1024])
+def test_grouped_on_pairs(K, silu):
+    """40 experts with all kinds of row counts, rows before the first and behind
+    the last left alone; twice the same bits."""
+    counts = [0, 1, 15, 16, 17, 32, 33, 191, 192, 193, 0, 0, 383, 384, 385, 700, 96, 97, 31, 2] * 2
+    offs = [7]
+    for c in counts:
+        offs.append(offs[-1] + c)
+    rows, E = offs[-1] + 29, len(counts)
+    a, w = make(rows, K, 352, E, K, 0.5)
+    off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    before = torch.randn(rows, 176 if silu else 352, device="cuda").bfloat16()
+    out = mx.matmul(a, w, off, silu_mul=silu, out=before.clone())
+    check_matmul(out, a, w, offs, silu, before)
+    assert torch.equal(out, mx.matmul(a, w, off, silu_mul=silu, out=before.clone()))
+    assert mx.status() == 0
+
+
+def test_pairs_offsets_and_bad_blocks():
+    a, w = make(6000, 128, 64, 60, 2)
+    for offs in ([6000 - 100 * i for i in range(61)], [0] + [6000, 0] * 30,
+                 [2 ** 31 - 1, -2 ** 31] * 30 + [50], [5900] + [10 ** 6] * 60):
+        guard = torch.zeros(8000, 64, device="cuda", dtype=torch.bfloat16)
+        mx.matmul(a, w, torch.tensor(offs, dtype=torch.int32, device="cuda"), out=guard[1000:7000])
+        torch.cuda.synchronize()
+        assert not guard[:1000].any() and not guard[7000:].any()
+    assert mx.status() == 0
+    a, w = make(1500, 512, 2304, 0, 3)
+    a.scales[7, 2] = 255
+    w.scales[1300, 0] = 255
+    nan = torch.isnan(mx.matmul(a, w))
+    want = torch.zeros_like(nan)
+    want[7], want[:, 1300] = True, True
+    assert torch.equal(nan, want)
+
+
+def test_scales_off_16_bytes():
+    """Scale arrays that TMA cannot address (their start, not their pitch)."""
+    a, w = make(1500, 512, 2304, 0, 9, 1.0)
+    def off(t):
+        buf = torch.empty(t.numel() + 16, dtype=torch.uint8, device="cuda")
+        v = buf[4:4 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+    b, v = mx.MxTensor(a.codes, off(a.scales)), mx.MxTensor(w.codes, off(w.scales))
+    for x, y in ((b, v), (a, v), (b, w)):
+        assert torch.equal(mx.matmul(x, y), mx.matmul(a, w))
+        few = mx.MxTensor(x.codes[:9], x.scales[:9])
+        assert torch.equal(mx.matmul(few, y), mx.matmul(mx.MxTensor(a.codes[:9], a.scales[:9]), w))
+
+
 def test_empty_batch_and_shapes():
     a, w = make(4, 128, 64, 3, 1)
     none = mx.MxTensor(a.codes[:0], a.scales[:0])
@@ -261,9 +324,10 @@ def test_other_stream_and_graph():
         check_matmul(gy, gq, w, off.tolist(), True, torch.zeros_like(gy))
 
 
-def test_two_streams_at_once():
-    a, w = make(700, 512, 256, 4, 6)
-    offs = [[0, 100, 300, 301, 700], [0, 0, 0, 690, 700]]
+@pytest.mark.parametrize("rows,N", [(700, 256), (5000, 2048)])
+def test_two_streams_at_once(rows, N):
+    a, w = make(rows, 512, N, 4, 6)
+    offs = [[0, 100, 300, 301, rows], [0, 0, 0, 690, rows]]
     off = [torch.tensor(o, dtype=torch.int32, device="cuda") for o in offs]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
