@@ -632,15 +632,24 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     pdl_trigger();
     pdl_wait();
     if (warp == 0) {
-        // the plan: offsets brought into [0, rows], and the prefix of row tiles
+        // the plan: offsets brought into [0, rows], and the prefix of row tiles;
+        // all offsets are loaded at once (one memory round trip)
+        constexpr int kSets = (kMaxExperts + 32) / 32;
+        int off[kSets];
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+            const int i = u * 32 + lane;
+            off[u] = i > E ? 0 : !p.offsets ? (i == 0 ? 0 : p.rows) : min(max(p.offsets[i], 0), p.rows);
+        }
         int run = 0;
-        for (int i0 = 0; i0 <= E; i0 += 32) {
-            const int i = i0 + lane;
-            auto at = [&](int j) {
-                return p.offsets ? min(max(p.offsets[j], 0), p.rows) : j == 0 ? 0 : p.rows;
-            };
-            const int beg = i <= E ? at(i) : 0;
-            int tiles = i < E ? (max(at(i + 1) - beg, 0) + NT - 1) / NT : 0;
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+            if (u * 32 > E) break;
+            const int i = u * 32 + lane;
+            int next = __shfl_down_sync(0xffffffffu, off[u], 1);
+            const int first = __shfl_sync(0xffffffffu, off[u + 1 < kSets ? u + 1 : u], 0);
+            if (lane == 31) next = first;
+            const int tiles = i < E ? (max(next - off[u], 0) + NT - 1) / NT : 0;
             int x = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -649,7 +658,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             }
             if (i <= E) {
                 mts[i] = run + x - tiles;
-                offs[i] = beg;
+                offs[i] = off[u];
             }
             run += __shfl_sync(0xffffffffu, x, 31);
         }
