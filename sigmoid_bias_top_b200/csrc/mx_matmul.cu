@@ -12,28 +12,38 @@
 //     computed; padded columns are never stored.
 // A tile is one CTA's (few rows per expert) or shared by two CTAs
 // (cta_group::2): 256 weight rows, each CTA staging its own 128 of them and half
-// of the tile's rows, which the MMA reads from both; that halves what a row
-// costs each SM's shared memory, whose writes and reads bound large batches.
+// of the tile's rows, which the MMA reads from both.
 // A stage holds K = 512: two TMA boxes of 256 values (128 bytes of codes) per
-// operand in the 128-byte swizzle. The scales, four 4-byte words per row and
-// stage, the tensor core takes from TMEM: column c, lane r of every 32-lane
-// quarter holds the word of row 32 c + r. TMA brings a stage's 16 bytes of every
-// row to shared memory; four warps, one per quarter, read them (rows lane, lane
-// + 32, ...) and store the words, whose transpose is a matter of register names,
-// to their quarter (tcgen05.st). What was slower: loads of the words by warps
-// (a 16-byte load of 32 rows took 150 cycles of the load unit's time, 4-byte
-// cp.async 45), and copies from shared memory to TMEM (tcgen05.cp), which run
-// in the MMAs' pipe, 30 cycles for 128 words, 360 a stage where the MMAs need 768.
-// Scale rows that TMA cannot address (K % 512, unaligned) are loaded by the four
-// warps themselves.
-// Roles (512 threads): a thread of warp 0 loads the weights' codes, one of warp
-// 15 the rows', one of warp 1 issues the MMAs, warps 2..5 bring the scales,
-// warps 6..13 drain the accumulators (two in TMEM, so that a tile's epilogue
-// runs under the next tile's MMAs), warp 14 works out the CTA's items (expert,
-// weight tile, row tile; dealt out in a fixed order), 32 at a time, one a lane:
-// divisions and searches that would cost every other role 2000 cycles per item.
-// All waits are bounded (1 s) and report a time-out in the status word; the
-// kernel then drains its copies and MMAs, frees TMEM and returns.
+// operand in the 128-byte swizzle, and the scales. Pairs keep the weights in a
+// ring of their own: where all of K fits it (K <= 2048), the row tiles of a weight
+// tile, which a pair takes one after another, share one load of it.
+// The scales, four 4-byte words per row and stage, the tensor core takes from
+// TMEM: column c, lane r of every 32-lane quarter holds the word of row 32 c + r.
+// TMA brings a stage's 16 bytes of every row to shared memory; four warps, one
+// per quarter, read them (rows lane, lane + 32, ...) and store the words, whose
+// transpose is a matter of register names, to their quarter (tcgen05.st). What
+// was slower: loads of the words by warps (a 16-byte load of 32 rows took 150
+// cycles of the load unit's time, 4-byte cp.async 45), and copies from shared
+// memory to TMEM (tcgen05.cp), which run in the MMAs' pipe, 30 cycles for 128
+// words, 360 a stage where the MMAs need 768. Scale rows that TMA cannot address
+// (K % 512, unaligned) are loaded by the four warps themselves.
+// Roles (512 threads): a thread of warp 0 loads the weights, one of warp 15 the
+// rows, one of warp 1 issues the MMAs, warps 2..5 bring the scales to TMEM, warps
+// 6..13 drain the accumulators (two in TMEM, so that a tile's epilogue runs under
+// the next tile's MMAs), warp 14 works out the items (expert, weight tile, row
+// tile), 16 at a time, one a lane: divisions and searches that would cost every
+// other role 2000 cycles per item. All waits are bounded (1 s) and report a
+// time-out in the status word; the kernel then drains its copies and MMAs, frees
+// TMEM and returns.
+//
+// What bounds it. Few rows: the weights' stream from HBM; 128 rows of 64 experts,
+// gate/up (K 2048, I 1536): 35 us, 5.3 TB/s of it, about 4 us of them the launch's
+// own latencies. Many rows: the 1000 W power cap and the stages' handshakes; 32768
+// rows: 107 us in short runs (SMs at 1.6 GHz, MMAs in half of the cycles), 127 us
+// in long ones (1.4 GHz). The shared load of the weights took 6% off both; half
+// the tile's rows per SM (pairs), 7%; skipping the weights' loads altogether, as a
+// bound, 20%. One row tile's shape, 192 rows: two accumulators and the scales fill
+// TMEM (512 columns).
 #include <cooperative_groups.h>
 #include <stddef.h>
 
@@ -55,8 +65,10 @@ constexpr int A_BYTES = A_SUB * KSUB;
 constexpr int kEpiWarps = 8;
 constexpr int kScaleWarps = 4;        // one per 32-lane quarter of TMEM
 constexpr int kThreads = 32 * (4 + kScaleWarps + kEpiWarps);
-constexpr int kDeal = 32;             // items worked out at a time
+constexpr int kDeal = 16;             // items worked out at a time
 constexpr int kMaxStages = 4;
+constexpr int NA = 4;                 // weight stages
+constexpr int A_SLOT = A_BYTES + WM * 16;  // codes and scales
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;  // shared::cluster address in the pair's even CTA
 
@@ -72,25 +84,32 @@ struct Cfg {
     static constexpr int B_ROWS = kPair ? NT / 2 : NT;
     static constexpr int B_SUB = B_ROWS * SUBK / 2;
     static constexpr int B_BYTES = B_SUB * KSUB;
-    static constexpr int SF_BYTES = (WM + NT + 63) / 64 * 64 * 16;  // a stage's scales, 16 bytes a row
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
-    static constexpr int STAGES = kPair ? 3 : 4;
-    static constexpr int SF_COLS = KWORDS * (4 + 4 * NB);  // TMEM columns of a stage's scales
-    static constexpr int SF_SLOTS = kPair ? 2 : 4;         // sets of them
-    static constexpr int USED_COLS = 2 * NT + SF_SLOTS * SF_COLS;
+    static constexpr int B_SLOT = B_BYTES + (NT + 63) / 64 * 64 * 16;  // codes and scales
+    static constexpr int STAGES = kPair ? 3 : 4;       // of the rows
+    static constexpr int SLOTS_BYTES = NA * A_SLOT + STAGES * B_SLOT;
+    static constexpr int SFA_COLS = 4 * KWORDS;        // TMEM columns of a weight stage's scales
+    static constexpr int SFB_COLS = 4 * KWORDS * NB;   // of a row stage's
+    static constexpr int SF_SLOTS = kPair ? 2 : 4;     // sets of the latter
+    static constexpr int USED_COLS = 2 * NT + NA * SFA_COLS + SF_SLOTS * SFB_COLS;
     static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
     static constexpr int N_STEP = 16;                  // the MMA's N is a multiple of it
     static_assert(USED_COLS <= 512 && STAGES <= kMaxStages, "TMEM");
+    static_assert(kPair || (STAGES == NA && SF_SLOTS == NA), "one ring of stages");
     // a slot's last MMAs are waited for on their stage's barrier, which a later
     // stage must not have gone through again by then
     static_assert(SF_SLOTS <= STAGES, "slots");
-    static_assert(B_SUB % 1024 == 0 && SF_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(A_SLOT % 1024 == 0 && B_SUB % 1024 == 0 && B_SLOT % 1024 == 0, "swizzle atoms");
 };
 
 struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
-    uint64_t full[kMaxStages];    // codes and scales are in place
-    uint64_t empty[kMaxStages];   // the stage's MMAs are done
-    uint64_t scaled[kMaxStages];  // the stage's scales are in shared memory
+    // pairs, whose weight stages outlive an item; single CTAs move both operands
+    // on together and count the weights' loads on the rows' barriers
+    uint64_t fulla[NA];            // the weights' codes are in place
+    uint64_t scaleda[NA];          // their scales are in shared memory
+    uint64_t emptya[NA];           // the MMAs of all items that share them are done
+    uint64_t fullb[kMaxStages];    // the rows' codes and all scales are in place
+    uint64_t scaledb[kMaxStages];  // the rows' scales are in shared memory
+    uint64_t emptyb[kMaxStages];   // the stage's MMAs are done
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t dealt[2];            // a set of kDeal items is in place
@@ -303,9 +322,11 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int h) {
 }
 
 // Work item: weight rows from wrow on (tile wt of its expert), `rows` rows from
-// t0; rows == 0 ends the list.
-struct __align__(16) Item {
+// t0; first, last: of a run of items that share the weights' stages. rows == 0
+// ends the list.
+struct Item {
     int wrow, wt, t0, rows;
+    bool first, last;
 };
 
 __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
@@ -318,20 +339,21 @@ __device__ __forceinline__ int find_expert(const int32_t *mts, int E, int q) {
 }
 
 // Items run expert by expert, the row tiles of a weight tile one after another.
-__device__ __forceinline__ Item decode(int item, int NW, const int32_t *mts, const int32_t *offs,
-                                       int E, int N, int tile_outputs, int n_step) {
-    Item it;
+// A CTA (pair) takes the items [begin, end), packed for shared memory. reuse:
+// the row tiles of a weight tile share its stages.
+__device__ __forceinline__ int4 decode(int item, int begin, int end, bool reuse, int NW,
+                                       const int32_t *mts, const int32_t *offs, int E, int N,
+                                       int tile_outputs, int n_step) {
     const int e = find_expert(mts, E, item / NW);
     const int ntt = mts[e + 1] - mts[e];
     const int local = item - mts[e] * NW;
-    it.wt = local / ntt;
-    const int tt = local - it.wt * ntt;
+    const int wt = local / ntt, tt = local - wt * ntt;
     const int c = offs[e + 1] - offs[e];
     const int ts = ((c + ntt - 1) / ntt + n_step - 1) / n_step * n_step;
-    it.t0 = offs[e] + tt * ts;
-    it.rows = min(ts, c - tt * ts);
-    it.wrow = e * N + it.wt * tile_outputs;
-    return it;
+    const bool first = !reuse || tt == 0 || item == begin;
+    const bool last = !reuse || tt == ntt - 1 || item == end - 1;
+    return make_int4(e * N + wt * tile_outputs, wt, offs[e] + tt * ts,
+                     min(ts, c - tt * ts) | (first ? 1 << 16 : 0) | (last ? 1 << 17 : 0));
 }
 
 // The shared addresses of a barrier of Ctl, at base `bars` (that of the Ctl).
@@ -353,11 +375,13 @@ struct Walk {
         const int set = (i / kDeal) & 1;
         if (i % kDeal == 0 && !wait_bar(MX_BAR(dealt, set), (i / (2 * kDeal)) & 1u, ctl, status)) return false;
         const uint4 v = ld_shared(bars + static_cast<uint32_t>(sizeof(Ctl)) +
-                                  (set * kDeal + i % kDeal) * static_cast<uint32_t>(sizeof(Item)));
+                                  (set * kDeal + i % kDeal) * static_cast<uint32_t>(sizeof(int4)));
         it.wrow = static_cast<int>(v.x);
         it.wt = static_cast<int>(v.y);
         it.t0 = static_cast<int>(v.z);
-        it.rows = static_cast<int>(v.w);
+        it.rows = static_cast<int>(v.w & 0xffffu);
+        it.first = v.w >> 16 & 1u;
+        it.last = v.w >> 17 & 1u;
         if (i % kDeal == kDeal - 1) {
             if (kWarp) __syncwarp();
             if (!kWarp || (threadIdx.x & 31) == 0) arrive_bar(MX_BAR(taken, set));
@@ -409,8 +433,9 @@ __device__ __forceinline__ uint4 load_words(const uint8_t *src, size_t row, int 
 }
 
 // A scale warp: the words of the CTA's 128 weight rows (first output o_base of
-// the tile's) and of the tile's rows, stage by stage, to its TMEM quarter. Rows
-// past the tile's end have any scales; their products are never stored.
+// the tile's; once for a run of items) and of the tile's rows, stage by stage, to
+// its TMEM quarter. Rows past the tile's end have any scales; their products are
+// never stored.
 template <typename C, bool kPair, bool kSilu>
 __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, uint32_t bars,
                                              uint32_t smem, uint32_t tmem_sf, int NO, int o_base,
@@ -420,27 +445,35 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
     const uint32_t taddr = tmem_sf + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
     Walk<true> walk(ctl, bars, p.status);
     Item it;
-    int s = 0, slot = 0;       // of the rings of stages and of TMEM columns
-    int os = 0, warmup = C::SF_SLOTS;  // the stage that used the slot before, if one did
-    uint32_t ph = 0, oph = 0;
+    int as = 0, s = 0, slot = 0;       // of the rings of weight stages, row stages, TMEM columns
+    int os = 0, warmup = C::SF_SLOTS;  // the row stage that used the columns before, if one did
+    uint32_t aph = 0, ph = 0, oph = 0;
     while (walk.next(it)) {
         const int o_last = NO - 1 - it.wt * tile_outputs;
         for (int kb = 0; kb < nk; ++kb) {
             uint4 a[4], b[4 * C::NB];
+            const bool load_a = !kPair || it.first;
             if (p.sf_tma) {
-                if (!wait_bar(MX_BAR(scaled, s), ph, ctl, p.status)) return;
-                const uint32_t sf = smem + s * C::STAGE_BYTES + A_BYTES + C::B_BYTES + lane * 16;
+                if (kPair && it.first && !wait_bar(MX_BAR(scaleda, as), aph, ctl, p.status)) return;
+                if (!wait_bar(MX_BAR(scaledb, s), ph, ctl, p.status)) return;
+                const uint32_t sfa = smem + as * A_SLOT + A_BYTES + lane * 16;
+                const uint32_t sfb = smem + NA * A_SLOT + s * C::B_SLOT + C::B_BYTES + lane * 16;
+                if (load_a) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = ld_shared(sf + i * 512);
+                    for (int i = 0; i < 4; ++i) a[i] = ld_shared(sfa + i * 512);
+                }
 #pragma unroll
-                for (int i = 0; i < 4 * C::NB; ++i) b[i] = i < C::R ? ld_shared(sf + WM * 16 + i * 512) : b[0];
+                for (int i = 0; i < 4 * C::NB; ++i) b[i] = i < C::R ? ld_shared(sfb + i * 512) : b[0];
             } else {
+                if (load_a) {
+                    if (kPair && !wait_bar(MX_BAR(emptya, as), aph ^ 1u, ctl, p.status)) return;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // gate/up: 16 gate rows and their 16 up rows in turn
-                    const int o = min(o_base + (kSilu ? i * 16 + (lane & 15) : i * 32 + lane), o_last);
-                    a[i] = load_words(p.ws, static_cast<size_t>(it.wrow) + o + (kSilu && lane >= 16 ? NO : 0),
-                                      p.K, kb);
+                    for (int i = 0; i < 4; ++i) {
+                        // gate/up: 16 gate rows and their 16 up rows in turn
+                        const int o = min(o_base + (kSilu ? i * 16 + (lane & 15) : i * 32 + lane), o_last);
+                        a[i] = load_words(p.ws, static_cast<size_t>(it.wrow) + o + (kSilu && lane >= 16 ? NO : 0),
+                                          p.K, kb);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 4 * C::NB; ++i)
@@ -448,24 +481,28 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
                                                  p.K, kb)
                                     : b[0];
             }
-            // the MMAs that read the slot's last scales are done
+            // the MMAs that read the columns' last scales are done
             if (warmup > 0) {
                 --warmup;
             } else {
-                if (!wait_bar(MX_BAR(empty, os), oph, ctl, p.status)) return;
+                if (!wait_bar(MX_BAR(emptyb, os), oph, ctl, p.status)) return;
                 if (++os == C::STAGES) { os = 0; oph ^= 1u; }
             }
             tc_fence_after();
-            const uint32_t to = taddr + static_cast<uint32_t>(slot * C::SF_COLS);
+            if (load_a) {
+                // a weight stage's columns are free with the stage itself; those of
+                // single CTAs, whose SF_SLOTS are as many, with the rows'
+                store_words(taddr + static_cast<uint32_t>(as * C::SFA_COLS), a);
+                if (++as == NA) { as = 0; aph ^= 1u; }
+            }
+            store_words(taddr + static_cast<uint32_t>(NA * C::SFA_COLS + slot * C::SFB_COLS), b);
             if (++slot == C::SF_SLOTS) slot = 0;
-            store_words(to, a);
-            store_words(to + 4 * KWORDS, b);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if constexpr (kPair) arrive_leader(MX_BAR(full, s));
-                else arrive_bar(MX_BAR(full, s));
+                if constexpr (kPair) arrive_leader(MX_BAR(fullb, s));
+                else arrive_bar(MX_BAR(fullb, s));
             }
             if (++s == C::STAGES) { s = 0; ph ^= 1u; }
         }
@@ -512,14 +549,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // One warp's 32 accumulator columns (rows c0.. of the tile) x its 32 TMEM lanes
 // to out. The fragments hold gate (lanes 0..15) and up (16..31) of an output in
 // the same thread and register. bf16: pairs of rows are packed, stored
-// transposed to the warp's staging rows (one per row of the tile, kPitch apart:
-// no bank conflicts) and leave as 16-byte pieces; fp32 leaves from the
-// fragments, 32 bytes of four rows at a time.
+// transposed to the warp's staging rows (kSub rows of the tile at a time, kPitch
+// apart: no bank conflicts) and leave as 16-byte pieces, one a lane; fp32 leaves
+// from the fragments, 32 bytes of four rows at a time.
 template <bool kSilu, typename T>
 struct Drain {
     static constexpr int kOutputs = kSilu ? 16 : 32;   // per warp
+    static constexpr int kPieces = kOutputs / 8;       // 16-byte pieces of a row
+    static constexpr int kSub = 32 / kPieces;          // rows: one piece a lane
     static constexpr int kPitch = kOutputs * 2 + 16;   // bytes
-    static constexpr int kStage = sizeof(T) == 2 ? 32 * kPitch : 0;
+    static constexpr int kStage = sizeof(T) == 2 ? kSub * kPitch : 0;
 
     static __device__ __forceinline__ void run(uint32_t taddr, uint32_t stage, T *out, int f0, int NO,
                                                int lim, int lane) {
@@ -535,31 +574,31 @@ struct Drain {
                     silu_mul<sizeof(T) == 2>(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
         }
         if constexpr (sizeof(T) == 2) {
-            const uint32_t at = stage + lane * kPitch;
-#pragma unroll
-            for (int h = 0; h < kOutputs / 16; ++h) {
-                const uint32_t(&v)[16] = h ? hi : lo;
-                uint32_t q[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                stmatrix_x4_trans(at + h * 32, q[0], q[2], q[4], q[6]);
-                stmatrix_x4_trans(at + h * 32 + 16, q[1], q[3], q[5], q[7]);
-            }
-            __syncwarp();
-            constexpr int kPieces = kOutputs / 8;       // 16-byte pieces of a row
+            // fragment registers 4g, 4g + 1 are rows 8g.. of outputs 0..7, 4g + 2
+            // and 4g + 3 of outputs 8..15 (and hi of 16..31)
+            auto pair_of = [](const uint32_t(&v)[16], int i) {
+                return pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            };
+            const int m = lane >> 3;  // the 8 x 8 tile whose row this lane names
+            const uint32_t at = kSilu ? stage + ((m >> 1) * 8 + (lane & 7)) * kPitch + (m & 1) * 16
+                                      : stage + (lane & 7) * kPitch + m * 16;
+            const uint32_t from = stage + lane / kPieces * kPitch + (lane % kPieces) * 16;
             const int col = f0 + (lane % kPieces) * 8;  // NO % 16 == 0: all 8 outputs or none
-            uint4 v[kPieces];
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                v[i] = ld_shared(stage + (i * 32 + lane) / kPieces * kPitch + (lane % kPieces) * 16);
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int r = (i * 32 + lane) / kPieces;
+            for (int u = 0; u < 32 / kSub; ++u) {
+                if constexpr (kSilu)
+                    stmatrix_x4_trans(at, pair_of(lo, 4 * u), pair_of(lo, 4 * u + 1), pair_of(lo, 4 * u + 2),
+                                      pair_of(lo, 4 * u + 3));
+                else
+                    stmatrix_x4_trans(at, pair_of(lo, 2 * u), pair_of(lo, 2 * u + 1), pair_of(hi, 2 * u),
+                                      pair_of(hi, 2 * u + 1));
+                __syncwarp();
+                const uint4 v = ld_shared(from);
+                const int r = u * kSub + lane / kPieces;
                 if (r < lim && col < NO)
-                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(r) * NO + col) = v[i];
+                    *reinterpret_cast<uint4 *>(out + static_cast<size_t>(r) * NO + col) = v;
+                __syncwarp();  // the staging rows are read before the next are written
             }
-            __syncwarp();  // the staging rows are read before the next chunk's are written
         } else {
 #pragma unroll
             for (int h = 0; h < kOutputs / 16; ++h) {
@@ -591,9 +630,9 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *stages_out = smem + C::STAGES * C::STAGE_BYTES;  // the epilogue's staging rows
+    uint8_t *stages_out = smem + C::SLOTS_BYTES;           // the epilogue's staging rows
     Ctl *ctl = reinterpret_cast<Ctl *>(stages_out + kEpiWarps * Drain<kSilu, T>::kStage);
-    Item *items = reinterpret_cast<Item *>(ctl + 1);       // [2][kDeal]
+    int4 *items = reinterpret_cast<int4 *>(ctl + 1);       // [2][kDeal]
     int32_t *mts = reinterpret_cast<int32_t *>(items + 2 * kDeal);  // [E+1] prefix of row tiles
     int32_t *offs = mts + (p.E + 1);                        // [E+1]
     const uint32_t base = smem_u32(smem), bars = smem_u32(ctl);
@@ -604,10 +643,16 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            // the two TMA threads (of the leader), the scale warps (of both CTAs)
-            mbar_init(&ctl->full[s], 2 + kCtas * kScaleWarps);
-            mbar_init(&ctl->scaled[s], 2);  // the two TMA threads
-            mbar_init(&ctl->empty[s], 1);
+            // the rows' TMA thread (of the leader; both of a single CTA), the scale
+            // warps (of both CTAs)
+            mbar_init(&ctl->fullb[s], (kPair ? 1 : 2) + kCtas * kScaleWarps);
+            mbar_init(&ctl->scaledb[s], kPair ? 1 : 2);
+            mbar_init(&ctl->emptyb[s], 1);
+        }
+        for (int s = 0; s < NA; ++s) {
+            mbar_init(&ctl->fulla[s], 1);  // the weights' TMA thread (of the leader)
+            mbar_init(&ctl->scaleda[s], 1);
+            mbar_init(&ctl->emptya[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl->tfull[b], 1);
@@ -676,55 +721,79 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     const int NW = (NO + kOutputs - 1) / kOutputs;
     const int nk = (p.K + BK - 1) / BK;
     const int total = mts[E] * NW;  // out fits in memory: far below 2^31
+    // a run's weights stay in shared memory where all their stages fit
+    const bool reuse = kPair && nk <= NA;
+    // a pair takes a block of items, which holds the runs together; a single CTA
+    // every gridDim.x-th one
+    const int crew = gridDim.x / kCtas, member = blockIdx.x / kCtas;
+    const int begin = kPair ? static_cast<int>(static_cast<int64_t>(total) * member / crew) : member;
+    const int end = kPair ? static_cast<int>(static_cast<int64_t>(total) * (member + 1) / crew) : total;
 
     if (warp == 0 || warp == kThreads / 32 - 1) {
         if (elect_one()) {
             // ----------- TMA producers: the weights', the rows' -----------
             const bool weights = warp == 0;
+            const int stages = weights ? NA : C::STAGES;
             int s = 0;
             uint32_t ph = 0;
-            bool issued[C::STAGES];
-            uint32_t issued_parity[C::STAGES];
-            for (int i = 0; i < C::STAGES; ++i) issued[i] = false;
+            bool issued[kMaxStages];
+            uint32_t issued_parity[kMaxStages];
+            for (int i = 0; i < kMaxStages; ++i) issued[i] = false;
             bool ok = true;
             Walk<false> walk(ctl, bars, p.status);
             Item it;
             while (ok && walk.next(it)) {
+                if (kPair && weights && !it.first) continue;
                 const int wrow = it.wrow + half * kCtaOutputs;
                 const int trow = it.t0 + half * (mma_n<C>(it) / 2);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(MX_BAR(empty, s), ph ^ 1u, ctl, p.status)) { ok = false; break; }
-                    const uint32_t sa = base + s * C::STAGE_BYTES, full = MX_BAR(full, s);
-                    if (leader) arrive_bar_tx(full, kCtas * (weights ? A_BYTES : C::B_BYTES));
-                    // the maps count two-byte columns: 64 of them are a box; what lies
-                    // past K arrives as zeros
-#pragma unroll
-                    for (int j = 0; j < KSUB; ++j) {
-                        const int x = (kb * KSUB + j) * 64;
-                        if (!weights) X::load_2d(sa + A_BYTES + j * C::B_SUB, &tmA, x, trow, full);
-                        else if (kSilu) X::load_4d(sa + j * A_SUB, &tmW, x, wrow / 16, full);
-                        else X::load_2d(sa + j * A_SUB, &tmW, x, wrow, full);
+                    if (!wait_bar(kPair && weights ? MX_BAR(emptya, s) : MX_BAR(emptyb, s), ph ^ 1u, ctl, p.status)) {
+                        ok = false;
+                        break;
                     }
-                    if (p.sf_tma) {  // every CTA its own weight rows' scales and all of the tile's rows'
-                        const uint32_t sf = sa + A_BYTES + C::B_BYTES, scaled = MX_BAR(scaled, s);
-                        arrive_bar_tx(scaled, (weights ? WM : NT) * 16);
-                        if (!weights) Tc<false>::load_2d(sf + WM * 16, &tmSA, kb * 8, it.t0, scaled);
-                        else if (kSilu) Tc<false>::load_4d(sf, &tmSW, kb * 8, wrow / 16, scaled);
-                        else Tc<false>::load_2d(sf, &tmSW, kb * 8, wrow, scaled);
+                    // the maps count two-byte columns: 64 of them are a box; what lies
+                    // past K arrives as zeros. Scales: every CTA its own weight rows'
+                    // and all of the tile's rows'
+                    const int x = kb * KSUB * 64;
+                    if (weights) {
+                        const uint32_t sa = base + s * A_SLOT, full = kPair ? MX_BAR(fulla, s) : MX_BAR(fullb, s),
+                                       scaled = kPair ? MX_BAR(scaleda, s) : MX_BAR(scaledb, s);
+                        if (leader) arrive_bar_tx(full, kCtas * A_BYTES);
+#pragma unroll
+                        for (int j = 0; j < KSUB; ++j) {
+                            if (kSilu) X::load_4d(sa + j * A_SUB, &tmW, x + j * 64, wrow / 16, full);
+                            else X::load_2d(sa + j * A_SUB, &tmW, x + j * 64, wrow, full);
+                        }
+                        if (p.sf_tma) {
+                            arrive_bar_tx(scaled, WM * 16);
+                            if (kSilu) Tc<false>::load_4d(sa + A_BYTES, &tmSW, kb * 8, wrow / 16, scaled);
+                            else Tc<false>::load_2d(sa + A_BYTES, &tmSW, kb * 8, wrow, scaled);
+                        }
+                    } else {
+                        const uint32_t sb = base + NA * A_SLOT + s * C::B_SLOT, full = MX_BAR(fullb, s),
+                                       scaled = MX_BAR(scaledb, s);
+                        if (leader) arrive_bar_tx(full, kCtas * C::B_BYTES);
+#pragma unroll
+                        for (int j = 0; j < KSUB; ++j) X::load_2d(sb + j * C::B_SUB, &tmA, x + j * 64, trow, full);
+                        if (p.sf_tma) {
+                            arrive_bar_tx(scaled, NT * 16);
+                            Tc<false>::load_2d(sb + C::B_BYTES, &tmSA, kb * 8, it.t0, scaled);
+                        }
                     }
                     issued[s] = true;
                     issued_parity[s] = ph;
-                    if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == stages) { s = 0; ph ^= 1u; }
                 }
             }
             // (a pair's copies complete on the leader's barriers)
             if (!ok || aborted(ctl)) {  // let the other roles leave and our own copies land
                 atomicExch(&ctl->abort, 1);
                 const uint64_t dl = globaltimer_ns() + kWaitNs;
-                for (int i = 0; i < C::STAGES; ++i)
+                for (int i = 0; i < stages; ++i)
                     if (issued[i]) {
-                        if (leader) mbar_wait(&ctl->full[i], issued_parity[i], dl);
-                        if (p.sf_tma) mbar_wait(&ctl->scaled[i], issued_parity[i], dl);
+                        const bool a = kPair && weights;
+                        if (leader) mbar_wait(a ? &ctl->fulla[i] : &ctl->fullb[i], issued_parity[i], dl);
+                        if (p.sf_tma) mbar_wait(a ? &ctl->scaleda[i] : &ctl->scaledb[i], issued_parity[i], dl);
                     }
             }
         }
@@ -733,7 +802,8 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             // ----------------------------- MMA ------------------------------
             const uint32_t desc0 = desc_low(base);
             int s = 0, tile = 0, slot = 0;
-            uint32_t ph = 0;
+            int run_as = 0;               // first weight stage of the run
+            uint32_t ph = 0, run_aph = 0;
             bool any = false;
             Walk<false> walk(ctl, bars, p.status);
             Item it;
@@ -746,13 +816,16 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 const int n = mma_n<C>(it);
                 const uint32_t idesc[2] = {idesc_mxf4(kCtas * WM, n, 0), idesc_mxf4(kCtas * WM, n, 1)};
                 bool ok = true;
+                int as = run_as;
+                uint32_t aph = run_aph;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(MX_BAR(full, s), ph, ctl, p.status)) { ok = false; break; }
+                    if (kPair && it.first && !wait_bar(MX_BAR(fulla, as), aph, ctl, p.status)) { ok = false; break; }
+                    if (!wait_bar(MX_BAR(fullb, s), ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = desc0 + static_cast<uint32_t>(s) * (C::STAGE_BYTES / 16);
-                    const uint32_t b0 = a0 + A_BYTES / 16;
-                    const uint32_t ta = tmem_sf + static_cast<uint32_t>(slot * C::SF_COLS);
-                    const uint32_t tb = ta + 4 * KWORDS;
+                    const uint32_t a0 = desc0 + static_cast<uint32_t>(as) * (A_SLOT / 16);
+                    const uint32_t b0 = desc0 + (NA * A_SLOT + static_cast<uint32_t>(s) * C::B_SLOT) / 16;
+                    const uint32_t ta = tmem_sf + static_cast<uint32_t>(as * C::SFA_COLS);
+                    const uint32_t tb = tmem_sf + static_cast<uint32_t>(NA * C::SFA_COLS + slot * C::SFB_COLS);
 #pragma unroll
                     for (int kk = 0; kk < BK / UK; ++kk)
                         X::mma(d_tmem, a0 + ((kk >> 2) * A_SUB + (kk & 3) * (UK / 2)) / 16,
@@ -760,11 +833,17 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                                ta + 4 * (kk >> 1), tb + 4 * C::NB * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
                     if (++slot == C::SF_SLOTS) slot = 0;
                     any = true;
-                    X::commit(MX_BAR(empty, s));
+                    X::commit(MX_BAR(emptyb, s));
+                    if (kPair && it.last) X::commit(MX_BAR(emptya, as));
                     if (++s == C::STAGES) { s = 0; ph ^= 1u; }
+                    if (++as == NA) { as = 0; aph ^= 1u; }
                 }
                 if (!ok) break;
                 X::commit(MX_BAR(tfull, buf));
+                if (it.last) {
+                    run_as = as;
+                    run_aph = aph;
+                }
             }
             if (any) {
                 X::commit_here(MX_BAR(drain, 0));
@@ -778,15 +857,14 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
         // ------------------------- item dealer --------------------------
         for (int c = 0;; ++c) {
             if (c >= 2 && !wait_bar(MX_BAR(taken, c & 1), ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
-            const int64_t item = blockIdx.x / kCtas +
-                                 (static_cast<int64_t>(c) * kDeal + lane) * (gridDim.x / kCtas);
-            Item it = {0, 0, 0, 0};
-            if (item < total)
-                it = decode(static_cast<int>(item), NW, mts, offs, E, p.N, kOutputs, C::N_STEP);
-            items[(c & 1) * kDeal + lane] = it;
+            const int64_t item = begin + (static_cast<int64_t>(c) * kDeal + lane) * (kPair ? 1 : crew);
+            int4 it = make_int4(0, 0, 0, 0);
+            if (lane < kDeal && item < end)
+                it = decode(static_cast<int>(item), begin, end, reuse, NW, mts, offs, E, p.N, kOutputs, C::N_STEP);
+            if (lane < kDeal) items[(c & 1) * kDeal + lane] = it;
             __syncwarp();
             if (lane == 0) arrive_bar(MX_BAR(dealt, c & 1));
-            if (__any_sync(0xffffffffu, it.rows == 0) || aborted(ctl)) break;
+            if (__any_sync(0xffffffffu, lane < kDeal && it.w == 0) || aborted(ctl)) break;
         }
     } else {
         // --------------------------- epilogue ---------------------------
@@ -917,8 +995,8 @@ int launch(const MxMatmulParams &args, int n_sm, cudaStream_t s) {
             (rc = encode_scales(&sa, p.as, p.rows, pitch, NT, 0)) != MOE_OK)
             return rc;
     }
-    const size_t smem = 1024 + C::STAGES * C::STAGE_BYTES + kEpiWarps * Drain<kSilu, T>::kStage +
-                        sizeof(Ctl) + 2 * kDeal * sizeof(Item) + 2 * (p.E + 1) * sizeof(int32_t);
+    const size_t smem = 1024 + C::SLOTS_BYTES + kEpiWarps * Drain<kSilu, T>::kStage +
+                        sizeof(Ctl) + 2 * kDeal * sizeof(int4) + 2 * (p.E + 1) * sizeof(int32_t);
     // no more CTAs than there can be items
     const int64_t items = static_cast<int64_t>(p.rows / NT + p.E) *
                           ((p.N + (kPair ? 2 : 1) * WM - 1) / ((kPair ? 2 : 1) * WM));
