@@ -13,8 +13,9 @@
  * scales[rows][K/32].
  *
  * All pointers are DEVICE pointers. The calls are asynchronous on `stream`,
- * allocate nothing and can be captured in a CUDA graph; the device must be the
- * calling thread's current one. Outputs must not overlap inputs.
+ * allocate nothing and can be captured in a CUDA graph (a device's first call of
+ * a kind sets its kernel up: make that one before a capture); the device must be
+ * the calling thread's current one. Outputs must not overlap inputs.
  */
 #ifndef SIGMOID_BIAS_TOP_MX_H
 #define SIGMOID_BIAS_TOP_MX_H
@@ -34,8 +35,8 @@ extern "C" {
  * saturate: the exponent follows amax alone, as the specification has it). A
  * block of zeros gets s = 0; a block that holds an infinity or a NaN gets
  * s = 255 and zero codes, so that its values are NaN. K % 32 == 0; x 16-byte
- * aligned and ld a multiple of 16 bytes; codes 16-byte and scales 4-byte
- * aligned. rows == 0 is a no-op. */
+ * aligned and ld a multiple of 16 bytes; codes 16-byte aligned. rows == 0 is a
+ * no-op. */
 int moe_mx_quantize(const void *x, int dtype, int64_t rows, int K, int64_t ld, uint8_t *codes,
                     uint8_t *scales, void *stream);
 

@@ -63,34 +63,35 @@ class _BalanceLoss(torch.autograd.Function):
         k, dev = idx.shape[1], logits.device
         B = 1 if seq_offsets is None else seq_offsets.numel() - 1
         L = lib()
-        both = logits.new_empty(2, dtype=torch.float32)   # loss, scale
+        loss = logits.new_empty((), dtype=torch.float32)
+        scale = logits.new_empty((), dtype=torch.float32)
         counts = idx.new_empty((B, E))
         prob = logits.new_empty((B, E), dtype=torch.float32)
         ws = idx.new_empty((L.moe_balance_workspace(n, E, B) + 3) // 4)
-        ptr = both.data_ptr()
         _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
                                      idx.data_ptr(), _ptr(seq_offsets), n, E, k, B, coef, eps,
-                                     ws.data_ptr(), ptr, counts.data_ptr(), prob.data_ptr(),
-                                     ptr + 4, _raw_stream(dev.index)), "moe_balance_forward")
-        ctx.save_for_backward(logits, counts, both, seq_offsets)
+                                     ws.data_ptr(), loss.data_ptr(), counts.data_ptr(),
+                                     prob.data_ptr(), scale.data_ptr(), _raw_stream(dev.index)),
+               "moe_balance_forward")
+        ctx.save_for_backward(logits, counts, scale, seq_offsets)
         ctx.k, ctx.eps = k, eps
         ctx.mark_non_differentiable(counts, prob)
         ctx.set_materialize_grads(False)
-        return both[0], counts, prob
+        return loss, counts, prob
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_loss, _counts, _prob):
         if grad_loss is None:
             return None, None, None, None, None
-        logits, counts, both, seq_offsets = ctx.saved_tensors
+        logits, counts, scale, seq_offsets = ctx.saved_tensors
         n, E = logits.shape
         dev = logits.device
         grad = logits.new_empty((n, E))
         # autograd runs this with the forward call's device and stream current
         _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
                                           counts.data_ptr(), _ptr(seq_offsets),
-                                          both.data_ptr() + 4, grad_loss.data_ptr(), n, E, ctx.k,
+                                          scale.data_ptr(), grad_loss.data_ptr(), n, E, ctx.k,
                                           counts.shape[0], ctx.eps, grad.data_ptr(),
                                           _raw_stream(dev.index)), "moe_balance_backward")
         return grad, None, None, None, None

@@ -720,7 +720,8 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     constexpr int kOutputs = kCtaOutputs * kCtas;          // outputs of a tile
     const int NW = (NO + kOutputs - 1) / kOutputs;
     const int nk = (p.K + BK - 1) / BK;
-    const int total = mts[E] * NW;  // out fits in memory: far below 2^31
+    // an out that fits in memory has far fewer tiles; offsets out of order may not
+    const int total = static_cast<int>(min(static_cast<int64_t>(mts[E]) * NW, INT64_C(0x7fffffff)));
     // a run's weights stay in shared memory where all their stages fit
     const bool reuse = kPair && nk <= NA;
     // a pair takes a block of items, which holds the runs together; a single CTA

@@ -223,7 +223,7 @@ static int check_rows(const void *x, int dtype, int64_t rows, int K, const void 
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return MOE_OK;
     if (!x || !codes || !scales) return MOE_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_ALIGNMENT;
+    if (!aligned(x, 16) || !aligned(codes, 16)) return MOE_ERR_ALIGNMENT;
     return MOE_OK;
 }
 

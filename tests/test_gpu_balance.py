@@ -126,6 +126,88 @@ def test_extreme_logits():
         check(r, grad, ref_logits, idx, [0, 6, 12], 1.0, eps)
 
 
+def test_tokens_of_no_sequence_may_hold_anything():
+    """NaN, infinities and the types' lowest values before the first sequence and
+    behind the last reach neither the loss nor a gradient."""
+    for dtype in ("f32", "bf16"):
+        for E in (16, 37, 256):
+            logits, idx = make(70, E, 4, dtype, E)
+            logits[:7], logits[60:] = float("nan"), float("inf")
+            logits[65:] = torch.finfo(DT[dtype]).min
+            idx[:7] = -1
+            logits.requires_grad_()
+            r = balance.balance_loss(logits, idx, offs(7, 30, 30, 60), coef=2.0)
+            grad, = torch.autograd.grad(r.loss, logits)
+            assert torch.isfinite(r.loss) and torch.isfinite(r.prob).all()
+            assert not grad[:7].any() and not grad[60:].any()
+            check(r, grad[7:60], logits[7:60], idx[7:60], [0, 23, 23, 53], 2.0, 1e-6)
+
+
+def test_a_bad_token_stays_in_its_sequence():
+    logits, idx = make(50, 32, 4, "f32")
+    logits[12, 3] = float("nan")
+    logits.requires_grad_()
+    r = balance.balance_loss(logits, idx, offs(0, 20, 50))
+    grad, = torch.autograd.grad(r.loss, logits)
+    assert torch.isnan(r.loss) and torch.isnan(r.prob[0]).all()
+    assert torch.isfinite(r.prob[1]).all() and torch.isnan(grad[12]).all()
+    rest = [t for t in range(50) if t != 12]
+    assert torch.isfinite(grad[rest]).all()
+
+
+def test_loss_is_an_ordinary_tensor():
+    """Added to in place, detached, without a gradient wanted; a second backward
+    of the backward is refused."""
+    logits, idx = make(20, 16, 2, "f32")
+    plain = balance.balance_loss(logits, idx)
+    assert not plain.loss.requires_grad
+    logits.requires_grad_()
+    r = balance.balance_loss(logits, idx, coef=0.5)
+    loss = r.loss
+    loss += (logits * logits).sum()
+    loss.backward()
+    alone, = torch.autograd.grad(balance.balance_loss(logits, idx, coef=0.5).loss, logits)
+    torch.testing.assert_close(logits.grad, alone + 2 * logits.detach(), rtol=1e-5, atol=1e-6)
+    assert not r.counts.requires_grad and not r.prob.requires_grad
+    g, = torch.autograd.grad(balance.balance_loss(logits, idx).loss, logits, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), logits)
+    with torch.no_grad():
+        assert torch.equal(balance.balance_loss(logits, idx).loss, plain.loss)
+
+
+def test_two_streams_at_once():
+    cases = [make(3000, 64, 4, "f32", i) for i in (1, 2)]
+    want = []
+    for logits, idx in cases:
+        logits.requires_grad_()
+        r = balance.balance_loss(logits, idx, offs(0, 1000, 3000))
+        want.append((r.loss.detach().clone(), torch.autograd.grad(r.loss, logits)[0].clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    o = offs(0, 1000, 3000)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (logits, idx) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                r = balance.balance_loss(logits, idx, o)
+                got.append((r.loss.detach(), torch.autograd.grad(r.loss, logits)[0]))
+    torch.cuda.synchronize()
+    for i, (loss, grad) in enumerate(got):
+        assert torch.equal(loss, want[i % 2][0]) and torch.equal(grad, want[i % 2][1])
+
+
+def test_many_sequences():
+    """More sequences than chunks, most of one token, some empty."""
+    n = 5000
+    logits, idx = make(n, 24, 3, "f32", 8)
+    cuts = torch.cat([torch.arange(0, 4000), torch.arange(4000, n, 7), torch.tensor([n, n, n])])
+    logits.requires_grad_()
+    r = balance.balance_loss(logits, idx, cuts.int().cuda())
+    check(r, torch.autograd.grad(r.loss, logits)[0], logits, idx, cuts.tolist(), 1.0, 1e-6)
+
+
 def test_strided_and_unaligned_logits():
     base = torch.randn(60, 100, device="cuda")
     for view in (base[:, :64], base[::2, 4:68], base[:, 1:65], base[:, 3:40], base.t()[:, :24],

@@ -67,7 +67,7 @@ def test_quantize_special_values(dtype):
 
 def test_quantize_strides_shapes_and_alignment():
     base = torch.randn(40, 320, generator=gen(), device="cuda")
-    for x in (base[:, :96], base[::2, 64:256], base.t()[:, :32], base[:, 2:66], base[3:4, :64],
+    for x in (base[0, :64], base[:, :96], base[::2, 64:256], base.t()[:, :32], base[:, 2:66], base[3:4, :64],
               base.view(5, 8, 320)[:, 2:5, :160], base.bfloat16()[:, 8:104]):
         q = mx.quantize(x)
         assert q.shape == tuple(x.shape)
@@ -78,6 +78,9 @@ def test_quantize_strides_shapes_and_alignment():
                       torch.zeros(40, 3, dtype=torch.uint8, device="cuda"))
     assert mx.quantize(base[:, :96], out=out) is not None
     check_quantized(out, base[:, :96])
+    q = mx.quantize(base[:, :96])
+    tail = mx.MxTensor(q.codes[7:], q.scales[7:])          # scales at an odd address
+    assert torch.equal(mx.dequantize(tail), mx.dequantize(q)[7:])
     empty = mx.quantize(base[:0, :64])
     assert empty.codes.shape == (0, 32) and mx.dequantize(empty).shape == (0, 64)
 
