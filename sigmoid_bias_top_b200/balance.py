@@ -56,6 +56,23 @@ def _ld(logits):
     return logits.stride(0) if logits.shape[0] > 1 else logits.shape[1]
 
 
+def _gradient(ctx, grad_loss):
+    logits, counts, scale, seq_offsets = ctx.saved_tensors
+    n, E = logits.shape
+    dev = logits.device
+    grad = logits.new_empty((n, E))
+    # autograd runs this with the forward call's device and stream current
+    _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
+                                      counts.data_ptr(), _ptr(seq_offsets),
+                                      scale.data_ptr(), grad_loss.data_ptr(), n, E, ctx.k,
+                                      counts.shape[0], ctx.eps, grad.data_ptr(),
+                                      _raw_stream(dev.index)), "moe_balance_backward")
+    return grad
+
+
+_once = once_differentiable(_gradient)
+
+
 class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, idx, seq_offsets, coef, eps):
@@ -80,20 +97,11 @@ class _BalanceLoss(torch.autograd.Function):
         return loss, counts, prob
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, grad_loss, _counts, _prob):
         if grad_loss is None:
             return None, None, None, None, None
-        logits, counts, scale, seq_offsets = ctx.saved_tensors
-        n, E = logits.shape
-        dev = logits.device
-        grad = logits.new_empty((n, E))
-        # autograd runs this with the forward call's device and stream current
-        _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
-                                          counts.data_ptr(), _ptr(seq_offsets),
-                                          scale.data_ptr(), grad_loss.data_ptr(), n, E, ctx.k,
-                                          counts.shape[0], ctx.eps, grad.data_ptr(),
-                                          _raw_stream(dev.index)), "moe_balance_backward")
+        # under create_graph, the wrapper that refuses a second derivative
+        grad = _once(ctx, grad_loss) if torch.is_grad_enabled() else _gradient(ctx, grad_loss)
         return grad, None, None, None, None
 
 

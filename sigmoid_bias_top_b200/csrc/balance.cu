@@ -21,6 +21,11 @@
 //   dloss/dl_e = (g_e - sum_j g_j p_j) / (sum s + eps) * s_e (1 - s_e),
 // a row at a time from its logits, which are read again: the scores cost less
 // to form than to store and load.
+//
+// 131072 tokens of 256 experts (fp32, 61 sequences): 37 us for the sums (3.7 TB/s;
+// 57 with one row in flight and full-precision exponentials), 8 for the last
+// reduction, 46 for the gradient (5.8 TB/s; 64 likewise). 64 tokens take 17 us on
+// the device, under the 100 that torch's autograd and the calls take on the host.
 #include "../../include/balance.h"
 #include "moe_internal.cuh"
 

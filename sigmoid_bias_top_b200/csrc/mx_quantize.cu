@@ -9,7 +9,8 @@
 // integers, NaN above infinity above every number), whose exponent field is
 // the block's floor(log2 amax); dividing by the scale is a multiplication by
 // a power of two and so exact, and the one rounding is that of the conversion
-// to E2M1.
+// to E2M1. 32768 x 2048 bf16: 30 us, 5.6 TB/s of the 6.5 that a copy reaches; the
+// way back takes 25 us.
 #include <cuda_fp16.h>
 
 #include "mx.cuh"
@@ -69,9 +70,10 @@ __device__ __forceinline__ Raw<kF32> load8(const void *x, int64_t elem) {
 }
 
 // kStrided: rows of x are ld elements apart; otherwise x is one run.
-// Six resident CTAs (42 registers) hide bf16's loads best: 33 us for 32768 x 2048
-// at five, 28 at six and 30 at eight; fp32, with twice the data in flight per
-// lane, loses what the spills cost.
+// Six resident CTAs (42 registers) hide bf16's loads best: quantising and
+// dequantising 32768 x 2048 takes 61.9 us at five, 55.8 at six and 57.7 at eight;
+// fp32, with twice the data in flight per lane, loses what the spills cost (4099 x
+// 1536: 15.1 us unlimited, 16.6 at six).
 template <bool kF32, bool kStrided>
 __global__ void __launch_bounds__(kThreads, kF32 ? 1 : 6)
     mx_quantize_kernel(const void *__restrict__ x, int64_t n, int K, int64_t ld,
