@@ -37,6 +37,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kFinishThreads = 1024;
 constexpr int kV = 8;               // experts per lane
 constexpr int kMinChunk = 8;        // tokens
+constexpr int kMaxChunk = 1024;     // tokens: a lane's fp32 sums stay under 128 terms
 constexpr int kMaxChunks = 148 * 4; // chunks of a large batch: four CTAs an SM
 
 struct FwdParams {
@@ -397,10 +398,10 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BwdParams p)
     }
 }
 
-// Tokens per chunk: enough chunks for every SM, at least kMinChunk tokens each.
+// Tokens per chunk: enough chunks for every SM, kMinChunk to kMaxChunk tokens each.
 int chunk_of(int N) {
-    int c = (N + kMaxChunks - 1) / kMaxChunks;
-    return c < kMinChunk ? kMinChunk : c;
+    const int c = static_cast<int>((static_cast<int64_t>(N) + kMaxChunks - 1) / kMaxChunks);
+    return c < kMinChunk ? kMinChunk : c > kMaxChunk ? kMaxChunk : c;
 }
 
 int lanes_per_row(int E) {

@@ -208,6 +208,16 @@ def test_many_sequences():
     check(r, torch.autograd.grad(r.loss, logits)[0], logits, idx, cuts.tolist(), 1.0, 1e-6)
 
 
+def test_long_batch():
+    """More tokens than the GPU has chunks for at their usual size."""
+    n = 650_000
+    logits, idx = make(n, 8, 2, "bf16", 4)
+    logits.requires_grad_()
+    cuts = (0, 3, n - 70_001, n)
+    r = balance.balance_loss(logits, idx, offs(*cuts))
+    check(r, torch.autograd.grad(r.loss, logits)[0], logits, idx, list(cuts), 1.0, 1e-6)
+
+
 def test_strided_and_unaligned_logits():
     base = torch.randn(60, 100, device="cuda")
     for view in (base[:, :64], base[::2, 4:68], base[:, 1:65], base[:, 3:40], base.t()[:, :24],

@@ -200,6 +200,19 @@ def test_grouped_on_pairs(K, silu):
     assert mx.status() == 0
 
 
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("mean", [4, 30, 60])
+def test_256_experts(mean, silu):
+    """The most experts there may be, for every tile size."""
+    g = torch.Generator().manual_seed(mean)
+    counts = torch.randint(0, 2 * mean + 1, (256,), generator=g)
+    counts[5] += 256 * mean - int(counts.sum()) if int(counts.sum()) < 256 * mean else 0
+    offs = [0] + counts.cumsum(0).tolist()
+    a, w = make(offs[-1], 640, 64, 256, mean, 0.5)
+    out = mx.matmul(a, w, torch.tensor(offs, dtype=torch.int32, device="cuda"), silu_mul=silu)
+    check_matmul(out, a, w, offs, silu)
+
+
 def test_pairs_offsets_and_bad_blocks():
     a, w = make(6000, 128, 64, 60, 2)
     for offs in ([6000 - 100 * i for i in range(61)], [0] + [6000, 0] * 30,
