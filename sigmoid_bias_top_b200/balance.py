@@ -18,7 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import MOE_BF16, MOE_F32, _check, lib as _moe_lib
-from .mx import _On, _here, _raw_stream
+from .mx import _INT, _On, _here, _raw_stream
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -113,7 +113,11 @@ def balance_loss(logits, idx, seq_offsets: Optional[torch.Tensor] = None, coef: 
     outside [0, E) are dropped slots and not counted), seq_offsets [B + 1] int32
     on the device (None: one sequence of all tokens); tokens of no sequence take
     no part and get a zero gradient. Runs on the current stream; the backward pass
-    on the stream that autograd gives it. E <= 256, k <= min(E, 8)."""
+    on the stream that autograd gives it. E <= 256, k <= min(E, 8).
+
+    In a CUDA graph, capture the forward and the backward pass together, with no
+    result of an eager call on the same leaves alive: autograd runs a leaf's last
+    step on the stream that first used it, and such a stream is not captured."""
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES:
         raise TypeError("logits must be a float32 or bfloat16 tensor")
     if logits.dim() != 2 or not logits.is_cuda:
@@ -127,6 +131,8 @@ def balance_loss(logits, idx, seq_offsets: Optional[torch.Tensor] = None, coef: 
             seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 2
             or not seq_offsets.is_contiguous() or seq_offsets.device != device):
         raise ValueError(f"seq_offsets must be a contiguous int32 (B + 1,) tensor on {device}")
+    if max(n, E, idx.shape[1]) >= _INT or seq_offsets is not None and seq_offsets.numel() > _INT:
+        raise ValueError("tokens, experts, slots and sequences must each be fewer than 2^31")
     if not _here(device, None):
         with _On(device, None):
             return balance_loss(logits, idx, seq_offsets, coef, eps)

@@ -17,6 +17,7 @@ import torch
 from . import MOE_BF16, MOE_F32, _check, lib as _moe_lib
 
 BLOCK = 32
+_INT = 1 << 31  # sizes pass as C ints, of which ctypes keeps the low 32 bits without a word
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
@@ -92,6 +93,8 @@ def _mx(name: str, q: MxTensor, least: int, most: int):
             or device != s.device):
         raise ValueError(f"{name}: codes [..., K/2] and scales [..., K/32] of one shape and device, "
                          f"got {tuple(cs)} and {tuple(ss)}")
+    if 2 * cs[-1] >= _INT:
+        raise ValueError(f"{name}: rows of fewer than 2^31 values, got {2 * cs[-1]}")
     return c, s, device
 
 
@@ -112,6 +115,8 @@ def quantize(x: torch.Tensor, out: Optional[MxTensor] = None, stream=None) -> Mx
     shape = x.shape
     if not x.is_cuda or len(shape) < 1 or shape[-1] == 0 or shape[-1] % BLOCK:
         raise ValueError("x must be a [..., K] CUDA tensor with K a multiple of 32")
+    if shape[-1] >= _INT:
+        raise ValueError(f"x must have rows of fewer than 2^31 values, got {shape[-1]}")
     device = x.device
     if not _here(device, stream):
         with _On(device, stream):
@@ -179,6 +184,8 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
     wc, ws, w_device = _mx("w", w, 2, 2) if offsets is None else _mx("w", w, 3, 3)
     rows, half = ac.shape
     N = wc.shape[-2]
+    if rows >= _INT or N >= _INT:
+        raise ValueError(f"fewer than 2^31 rows, got {rows} of a and {N} of w")
     if wc.shape[-1] != half or w_device != device:
         raise ValueError(f"w must hold rows of {2 * half} values on {device}")
     E, offs = 1, None

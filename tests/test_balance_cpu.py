@@ -58,3 +58,17 @@ def test_reference_gradient():
             num = (R.balance(l + d, idx, cuts, 0.7, 1e-3)["loss"]
                    - R.balance(l - d, idx, cuts, 0.7, 1e-3)["loss"]) / (2 * h)
             assert abs(float(num - ref["grad"][t, e])) < 1e-8
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Counts whose low 32 bits would look like a small one. The tensors have no
+    storage: nothing is allocated and nothing launched."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    big = (1 << 32) + 8
+    with FakeTensorMode():
+        def ints(*shape):
+            return torch.empty(*shape, dtype=torch.int32, device="cuda:0")
+        with pytest.raises(ValueError, match="2\\^31"):
+            balance.balance_loss(torch.empty(big, 1, device="cuda:0"), ints(big, 1))
+        with pytest.raises(ValueError, match="2\\^31"):
+            balance.balance_loss(torch.empty(8, 4, device="cuda:0"), ints(8, 1), ints(big))

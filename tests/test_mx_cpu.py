@@ -109,3 +109,21 @@ def test_mxfp4_layer_refusals():
                            ctypes.byref(h)) == -1
     assert L.moe_route_noalloc(256, sb.MOE_MXFP4, 256, 256, 256, 8, 256, 16, 4, 1e-6, 1.0, 256, 256,
                                None) == -1
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Widths whose low 32 bits would look like a small one. The tensors have no
+    storage: nothing is allocated and nothing launched."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    K = (1 << 32) + 128
+    with FakeTensorMode():
+        def q(*lead):
+            return mx.MxTensor(*(torch.empty(*lead, K // d, dtype=torch.uint8, device="cuda:0")
+                                 for d in (2, 32)))
+        for shape in ((K,), (2, K)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                mx.quantize(torch.empty(shape, dtype=torch.bfloat16, device="cuda:0"))
+        with pytest.raises(ValueError, match="2\\^31"):
+            mx.dequantize(q())
+        with pytest.raises(ValueError, match="2\\^31"):
+            mx.matmul(q(1), q(16))
