@@ -6,7 +6,8 @@
  * For logits l[n_tokens][E] and the experts idx[n_tokens][k] that the router
  * selected (moe_route_noalloc), with the sequences b that seq_offsets cuts the
  * tokens into, T_b tokens each:
- *   s_te = sigmoid(l_te),  p_te = s_te / (sum_j s_tj + eps)  (0 where that is 0)
+ *   s_te = sigmoid(l_te),  p_te = s_te / (sum_j s_tj + eps)  (0 where that is 0;
+ *     logits below -104, whose scores fp32 rounds to 0, have scores of 0)
  *   counts_be = number of slots of b's tokens that hold expert e
  *   f_be = E counts_be / (k T_b),  prob_be = mean over b's tokens of p_te
  *   loss = coef / B' * sum_b sum_e f_be prob_be,  B' = sequences with tokens

@@ -124,20 +124,52 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
 // v = sigmoid(v) per value; returns the row's sum of scores plus eps. slope, if
 // given, gets sigmoid's derivative: with t = exp(-|v|) it is t / (1 + t)^2,
 // which keeps its relative accuracy where 1 - s would cancel.
+// Shares and gradients only see scores, slopes and eps relative to the total, so
+// all may be in any common scale. Totals under kTiny, whose scores may be subnormal
+// and whose reciprocal may overflow, get the scale e^80: every logit of such a row
+// lies under -22, s and its derivative are exp(v) to 2^-31, and exp(v + 80) is an
+// ordinary number down to the -104 below which fp32 rounds a score to 0 (v + 80 is
+// exact). Only eps < kTiny can have them; the branch costs a compare otherwise, and
+// no registers, because it has the logits loaded again.
+constexpr float kTiny = 0x1p-32f;
+constexpr float kTinyShift = 80.f, kTinyScale = 5.5406223843935098e34f;  // e^80
+constexpr float kLowest = -104.f;
 template <int TPR>
-__device__ __forceinline__ float scores(float (&v)[kV], float eps, float *slope = nullptr) {
+__device__ __forceinline__ float row_sum(const float (&v)[kV]) {
     float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) sum += v[i];
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+template <int TPR, typename Reload>
+__device__ __forceinline__ float scores(float (&v)[kV], float eps, float *slope, Reload reload) {
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
         const float t = __expf(-fabsf(v[i]));
         const float r = __fdividef(1.0f, 1.0f + t);
         v[i] = v[i] < 0.f ? t * r : r;   // a NaN stays one through t
         if (slope) slope[i] = t * r * r;
-        sum += v[i];
     }
+    float total = row_sum<TPR>(v) + eps;
+    if (eps < kTiny && __any_sync(0xffffffffu, total < kTiny)) {
+        float u[kV];
+        reload(u);
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum + eps;
+        for (int i = 0; i < kV; ++i) u[i] = u[i] < kLowest ? 0.f : __expf(u[i] + kTinyShift);
+        const float scaled = row_sum<TPR>(u) + eps * kTinyScale;
+        if (total < kTiny) {
+            total = scaled;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                v[i] = u[i];
+                if (slope) slope[i] = u[i];
+            }
+        }
+    }
+    return total;
 }
 
 template <bool kF32, int TPR>
@@ -174,7 +206,9 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(FwdParams p) 
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int r = r0 + u * kWarps * G + grp;
-                const float total = scores<TPR>(v[u], p.eps);
+                const float total = scores<TPR>(v[u], p.eps, nullptr, [&](float (&l)[kV]) {
+                    load_logits<kF32>(p.logits, (r < stop ? r : r0) * p.ld, e0, p.E, p.vec, l);
+                });
                 if (r < stop) {
                     // eps may be 0 and every score may have underflowed: no share then
                     const float inv = total == 0.f ? 0.f : 1.0f / total;
@@ -357,7 +391,9 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BwdParams p)
             }
         }
         float slope[kV];
-        const float total = scores<TPR>(v, p.eps, slope);
+        const float total = scores<TPR>(v, p.eps, slope, [&](float (&l)[kV]) {
+            load_logits<kF32>(p.logits, (live ? r : 0) * p.ld, e0, p.E, p.vec, l);
+        });
         const float inv = total == 0.f ? 0.f : 1.0f / total;
         float dot = 0.f;
 #pragma unroll
