@@ -15,7 +15,6 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import MOE_BF16, MOE_F32, _check, lib as _moe_lib
 from .mx import _INT, _On, _here, _raw_stream
@@ -70,7 +69,18 @@ def _gradient(ctx, grad_loss):
     return grad
 
 
-_once = once_differentiable(_gradient)
+class _FirstOrder(torch.autograd.Function):
+    """grad as it is, as a function of what it was computed from whose derivative is
+    refused. A gradient without a graph would be a constant to a second
+    differentiation, which would then leave it out of a sum with other losses'."""
+
+    @staticmethod
+    def forward(ctx, grad, logits, grad_loss):
+        return grad
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("balance_loss has no second derivative")
 
 
 class _BalanceLoss(torch.autograd.Function):
@@ -100,8 +110,9 @@ class _BalanceLoss(torch.autograd.Function):
     def backward(ctx, grad_loss, _counts, _prob):
         if grad_loss is None:
             return None, None, None, None, None
-        # under create_graph, the wrapper that refuses a second derivative
-        grad = _once(ctx, grad_loss) if torch.is_grad_enabled() else _gradient(ctx, grad_loss)
+        grad = _gradient(ctx, grad_loss)
+        if torch.is_grad_enabled():  # create_graph
+            grad = _FirstOrder.apply(grad, ctx.saved_tensors[0], grad_loss)
         return grad, None, None, None, None
 
 
@@ -112,7 +123,8 @@ def balance_loss(logits, idx, seq_offsets: Optional[torch.Tensor] = None, coef: 
     logits [n, E] f32 or bf16 (rows may be strided), idx [n, k] int32 (values
     outside [0, E) are dropped slots and not counted), seq_offsets [B + 1] int32
     on the device (None: one sequence of all tokens); tokens of no sequence take
-    no part and get a zero gradient. Runs on the current stream; the backward pass
+    no part and get a zero gradient. There is no second derivative: asking for one
+    raises RuntimeError. Runs on the current stream; the backward pass
     on the stream that autograd gives it. E <= 256, k <= min(E, 8).
 
     In a CUDA graph, capture the forward and the backward pass together, with no
