@@ -53,8 +53,16 @@ int moe_balance_forward(const void *logits, int dtype, int64_t ld, const int32_t
                         int n_seqs, float coef, float eps, void *workspace, float *loss,
                         int32_t *counts, float *prob, float *scale, void *stream);
 
+/* The same, with the counts stored in kept[B][E] as well: for a backward pass whose
+ * caller changes counts meanwhile (a sum over ranks, say). */
+int moe_balance_forward_kept(const void *logits, int dtype, int64_t ld, const int32_t *idx,
+                             const int32_t *seq_offsets, int n_tokens, int n_experts, int top_k,
+                             int n_seqs, float coef, float eps, void *workspace, float *loss,
+                             int32_t *counts, float *prob, float *scale, int32_t *kept,
+                             void *stream);
+
 /* grad[n_tokens][E] (contiguous, dtype of the logits) = grad_loss[0] (device,
- * fp32) * dloss/dlogits, from the counts and scale of the forward call; 0 for
+ * fp32) * dloss/dlogits, from the counts (or kept) and scale of the forward call; 0 for
  * tokens of no sequence. */
 int moe_balance_backward(const void *logits, int dtype, int64_t ld, const int32_t *counts,
                          const int32_t *seq_offsets, const float *scale, const float *grad_loss,

@@ -24,7 +24,8 @@ _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 class Balance(NamedTuple):
     loss: torch.Tensor     # [] f32, differentiable with respect to the logits
-    counts: torch.Tensor   # [B, E] int32: slots of the sequence's tokens that hold the expert
+    counts: torch.Tensor   # [B, E] int32: slots of the sequence's tokens that hold the expert;
+                           # the caller's to change (the gradient does not read it)
     prob: torch.Tensor     # [B, E] f32: mean normalised score (no gradient)
 
 
@@ -40,6 +41,8 @@ def lib():
         L.moe_balance_workspace.restype = ctypes.c_size_t
         L.moe_balance_forward.argtypes = [P, I, I64, P, P, I, I, I, I, F, F, P, P, P, P, P, P]
         L.moe_balance_forward.restype = I
+        L.moe_balance_forward_kept.argtypes = L.moe_balance_forward.argtypes[:-1] + [P, P]
+        L.moe_balance_forward_kept.restype = I
         L.moe_balance_backward.argtypes = [P, I, I64, P, P, P, P, I, I, I, I, F, P, P]
         L.moe_balance_backward.restype = I
         _bound = True
@@ -56,15 +59,15 @@ def _ld(logits):
 
 
 def _gradient(ctx, grad_loss):
-    logits, counts, scale, seq_offsets = ctx.saved_tensors
+    logits, kept, seq_offsets = ctx.saved_tensors
     n, E = logits.shape
-    dev = logits.device
+    B, dev, counts = ctx.B, logits.device, kept.data_ptr()
     grad = logits.new_empty((n, E))
     # autograd runs this with the forward call's device and stream current
     _check(lib().moe_balance_backward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
-                                      counts.data_ptr(), _ptr(seq_offsets),
-                                      scale.data_ptr(), grad_loss.data_ptr(), n, E, ctx.k,
-                                      counts.shape[0], ctx.eps, grad.data_ptr(),
+                                      counts, _ptr(seq_offsets), counts + 4 * B * E,
+                                      grad_loss.data_ptr(), n, E, ctx.k, B, ctx.eps,
+                                      grad.data_ptr(),
                                       _raw_stream(dev.index)), "moe_balance_backward")
     return grad
 
@@ -91,17 +94,20 @@ class _BalanceLoss(torch.autograd.Function):
         B = 1 if seq_offsets is None else seq_offsets.numel() - 1
         L = lib()
         loss = logits.new_empty((), dtype=torch.float32)
-        scale = logits.new_empty((), dtype=torch.float32)
         counts = idx.new_empty((B, E))
+        # the backward pass's own counts (the caller may sum the others over ranks in
+        # place, which autograd does not see) and behind them its scale
+        kept = idx.new_empty(B * E + 1)
         prob = logits.new_empty((B, E), dtype=torch.float32)
         ws = idx.new_empty((L.moe_balance_workspace(n, E, B) + 3) // 4)
-        _check(L.moe_balance_forward(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
-                                     idx.data_ptr(), _ptr(seq_offsets), n, E, k, B, coef, eps,
-                                     ws.data_ptr(), loss.data_ptr(), counts.data_ptr(),
-                                     prob.data_ptr(), scale.data_ptr(), _raw_stream(dev.index)),
-               "moe_balance_forward")
-        ctx.save_for_backward(logits, counts, scale, seq_offsets)
-        ctx.k, ctx.eps = k, eps
+        own = kept.data_ptr()
+        _check(L.moe_balance_forward_kept(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits),
+                                          idx.data_ptr(), _ptr(seq_offsets), n, E, k, B, coef, eps,
+                                          ws.data_ptr(), loss.data_ptr(), counts.data_ptr(),
+                                          prob.data_ptr(), own + 4 * B * E, own,
+                                          _raw_stream(dev.index)), "moe_balance_forward")
+        ctx.save_for_backward(logits, kept, seq_offsets)
+        ctx.B, ctx.k, ctx.eps = B, k, eps
         ctx.mark_non_differentiable(counts, prob)
         ctx.set_materialize_grads(False)
         return loss, counts, prob

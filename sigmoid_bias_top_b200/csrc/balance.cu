@@ -49,7 +49,7 @@ struct FwdParams {
     double *seq_loss;   // [B]
     int32_t *ticket;    // finished CTAs of the second launch
     float *loss, *prob, *scale;
-    int32_t *counts;
+    int32_t *counts, *kept;  // kept: a second copy of counts, or null
     int N, E, k, B, chunk, nchunk;
     float coef, eps;
     bool vec;           // rows start on 16 bytes and E % 8 == 0
@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FwdParam
         const double prob = T > 0 ? s / T : 0.0;
         p.prob[static_cast<size_t>(b) * p.E + e] = static_cast<float>(prob);
         p.counts[static_cast<size_t>(b) * p.E + e] = n;
+        if (p.kept) p.kept[static_cast<size_t>(b) * p.E + e] = n;
         if (T > 0) mine = static_cast<double>(p.E) * n / (static_cast<double>(p.k) * T) * prob;
     }
     int none = 0;
@@ -501,11 +502,10 @@ extern "C" size_t moe_balance_workspace(int n_tokens, int n_experts, int n_seqs)
     return 256 + static_cast<size_t>(n_seqs) * 8 + slots * n_experts * 8;
 }
 
-extern "C" int moe_balance_forward(const void *logits, int dtype, int64_t ld, const int32_t *idx,
-                                   const int32_t *seq_offsets, int n_tokens, int n_experts,
-                                   int top_k, int n_seqs, float coef, float eps, void *workspace,
-                                   float *loss, int32_t *counts, float *prob, float *scale,
-                                   void *stream) {
+static int forward(const void *logits, int dtype, int64_t ld, const int32_t *idx,
+                   const int32_t *seq_offsets, int n_tokens, int n_experts, int top_k, int n_seqs,
+                   float coef, float eps, void *workspace, float *loss, int32_t *counts, float *prob,
+                   float *scale, int32_t *kept, void *stream) {
     int rc = check_shape(dtype, ld, seq_offsets, n_tokens, n_experts, top_k, n_seqs, eps);
     if (rc != MOE_OK) return rc;
     if (!workspace || !loss || !counts || !prob || !scale || (n_tokens > 0 && (!logits || !idx)))
@@ -522,7 +522,7 @@ extern "C" int moe_balance_forward(const void *logits, int dtype, int64_t ld, co
     p.seq_loss = reinterpret_cast<double *>(w + 256);
     p.part = reinterpret_cast<float *>(w + 256 + static_cast<size_t>(n_seqs) * 8);
     p.part_n = reinterpret_cast<int32_t *>(p.part + slots * n_experts);
-    p.loss = loss; p.counts = counts; p.prob = prob; p.scale = scale;
+    p.loss = loss; p.counts = counts; p.kept = kept; p.prob = prob; p.scale = scale;
     p.coef = coef; p.eps = eps;
     p.vec = rows_vec(logits, dtype, ld, n_experts);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -532,6 +532,26 @@ extern "C" int moe_balance_forward(const void *logits, int dtype, int64_t ld, co
         return MOE_ERR_CUDA;
     }
     return launch_k(balance_finish_kernel, dim3(n_seqs), dim3(kFinishThreads), 0, s, p);
+}
+
+extern "C" int moe_balance_forward(const void *logits, int dtype, int64_t ld, const int32_t *idx,
+                                   const int32_t *seq_offsets, int n_tokens, int n_experts,
+                                   int top_k, int n_seqs, float coef, float eps, void *workspace,
+                                   float *loss, int32_t *counts, float *prob, float *scale,
+                                   void *stream) {
+    return forward(logits, dtype, ld, idx, seq_offsets, n_tokens, n_experts, top_k, n_seqs, coef, eps,
+                   workspace, loss, counts, prob, scale, nullptr, stream);
+}
+
+extern "C" int moe_balance_forward_kept(const void *logits, int dtype, int64_t ld,
+                                        const int32_t *idx, const int32_t *seq_offsets,
+                                        int n_tokens, int n_experts, int top_k, int n_seqs,
+                                        float coef, float eps, void *workspace, float *loss,
+                                        int32_t *counts, float *prob, float *scale, int32_t *kept,
+                                        void *stream) {
+    if (!kept) return MOE_ERR_INVALID_ARG;
+    return forward(logits, dtype, ld, idx, seq_offsets, n_tokens, n_experts, top_k, n_seqs, coef, eps,
+                   workspace, loss, counts, prob, scale, kept, stream);
 }
 
 extern "C" int moe_balance_backward(const void *logits, int dtype, int64_t ld,

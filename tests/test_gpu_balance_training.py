@@ -1,5 +1,5 @@
 """The balance loss inside a training step: beside another loss under a second
-differentiation."""
+differentiation, and with its counts summed in place over ranks."""
 import pytest
 import torch
 
@@ -30,3 +30,20 @@ def test_a_second_derivative_is_refused_beside_other_losses():
     g, = torch.autograd.grad(balance.balance_loss(logits, idx).loss * coef, logits, create_graph=True)
     with pytest.raises(RuntimeError, match="second derivative"):
         torch.autograd.grad(g.sum(), coef)
+
+
+def test_counts_changed_before_the_backward_pass():
+    """A collective sums them in place without autograd's knowledge (.data does
+    the same here); the gradient is that of this rank's own counts."""
+    logits, idx = make(300, 64, 4)
+    for off in (None, torch.tensor([0, 100, 100, 290], dtype=torch.int32, device="cuda")):
+        r = balance.balance_loss(logits, idx, off)
+        want, = torch.autograd.grad(r.loss, logits)
+        r = balance.balance_loss(logits, idx, off)
+        r.counts.data.mul_(8)
+        r.prob.data.zero_()
+        got, = torch.autograd.grad(r.loss, logits)
+        assert torch.equal(got, want)
+        r = balance.balance_loss(logits, idx, off)
+        r.counts.add_(1)                           # known to autograd
+        assert torch.equal(torch.autograd.grad(r.loss, logits)[0], want)
