@@ -33,7 +33,8 @@ extern "C" {
 #endif
 
 /* Bytes of device workspace of moe_balance_forward (256-byte aligned; scratch
- * of one call: it may be reused once the call's kernels are done). */
+ * of one call: it may be reused once the call's kernels are done); 0 for token
+ * and sequence counts that it refuses. */
 size_t moe_balance_workspace(int n_tokens, int n_experts, int n_seqs);
 
 /* loss[1] fp32, counts[B][E] int32, prob[B][E] fp32 (0 for a sequence without
@@ -45,9 +46,9 @@ size_t moe_balance_workspace(int n_tokens, int n_experts, int n_seqs);
  * {0, n_tokens}. Tokens of no sequence do not take part. Offsets that do not
  * ascend within [0, n_tokens] give unspecified results, with no access
  * outside the buffers.
- * 1 <= E <= 256, 1 <= k <= min(E, 8), n_seqs >= 1, eps >= 0; n_tokens E and
- * n_seqs E below 2^31. All sums run in a fixed order: equal inputs give equal
- * bits. Device pointers, asynchronous on stream, no allocation. */
+ * 1 <= E <= 256, 1 <= k <= min(E, 8), n_seqs >= 1, eps >= 0; n_tokens and
+ * n_seqs below 2^30, n_tokens E and n_seqs E below 2^31. All sums run in a fixed
+ * order: equal inputs give equal bits. Device pointers, asynchronous on stream, no allocation. */
 int moe_balance_forward(const void *logits, int dtype, int64_t ld, const int32_t *idx,
                         const int32_t *seq_offsets, int n_tokens, int n_experts, int top_k,
                         int n_seqs, float coef, float eps, void *workspace, float *loss,

@@ -39,6 +39,8 @@ constexpr int kV = 8;               // experts per lane
 constexpr int kMinChunk = 8;        // tokens
 constexpr int kMaxChunk = 1024;     // tokens: a lane's fp32 sums stay under 128 terms
 constexpr int kMaxChunks = 148 * 4; // chunks of a large batch: four CTAs an SM
+constexpr int kMaxCount = 1 << 30;  // tokens, sequences: a chunk, a step or both together past the
+                                    // last one still fit an int
 
 struct FwdParams {
     const void *logits;
@@ -479,6 +481,7 @@ int check_shape(int dtype, int64_t ld, const void *seq, int N, int E, int k, int
     if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (N < 0 || B < 1 || !(eps >= 0.f) || (!seq && B != 1)) return MOE_ERR_INVALID_ARG;
     if (E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK || k > E) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (N >= kMaxCount || B >= kMaxCount) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(N) * E >= (INT64_C(1) << 31) ||
         static_cast<int64_t>(B) * E >= (INT64_C(1) << 31))
         return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -496,7 +499,8 @@ bool rows_vec(const void *logits, int dtype, int64_t ld, int E) {
 using namespace moe;
 
 extern "C" size_t moe_balance_workspace(int n_tokens, int n_experts, int n_seqs) {
-    if (n_tokens < 0 || n_experts < 1 || n_seqs < 1) return 0;
+    if (n_tokens < 0 || n_experts < 1 || n_seqs < 1 || n_tokens >= kMaxCount || n_seqs >= kMaxCount)
+        return 0;
     const int chunk = chunk_of(n_tokens);
     const size_t slots = static_cast<size_t>((n_tokens + chunk - 1) / chunk) + n_seqs;
     return 256 + static_cast<size_t>(n_seqs) * 8 + slots * n_experts * 8;
