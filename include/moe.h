@@ -95,7 +95,7 @@ typedef struct moe_ctx moe_ctx;
  *   MOE_F32: d % 4 == 0, any d_ff >= 1;
  *   MOE_BF16: d % 64 == 0, d_ff % 64 == 0 (tensor-core tiles);
  *   MOE_FP8_BLOCK: d % 128 == 0, d_ff % 128 == 0 (whole scale blocks);
- *   MOE_MXFP4: d % 128 == 0, d_ff % 128 == 0 (four scales).
+ *   MOE_MXFP4: d % 128 == 0, d_ff % 128 == 0 (four scales), d_ff <= 2^22.
  * On success *out receives the context; on failure *out is set to NULL and
  * nothing stays allocated. Synchronous. The workspace holds the grouped rows,
  * the expert intermediates and outputs of max_tokens * top_k assignments;

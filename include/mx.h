@@ -58,7 +58,7 @@ int moe_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
  * rounded once. Rows of no expert are left as they were. Offsets that do not
  * ascend within [0, rows] give unspecified rows, with no access outside the
  * buffers. An expert may have no rows; rows == 0 is a no-op.
- * K % 128 == 0, N % 16 == 0 (N % 32 == 0 with silu_mul), n_experts <= 256,
+ * K % 128 == 0, K <= 2^22, N % 16 == 0 (N % 32 == 0 with silu_mul), n_experts <= 256,
  * rows < 2^30 and n_experts * N < 2^30; codes and out 16-byte, scales and
  * offsets 4-byte aligned. */
 int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,

@@ -142,7 +142,8 @@ static int check_shapes(int d, int E, int I, int k, int dtype, int max_tokens) {
     if (dtype == MOE_BF16 && (d % 64 != 0 || I % 64 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (dtype == MOE_FP8_BLOCK && (d % kFp8Block != 0 || I % kFp8Block != 0))
         return MOE_ERR_UNSUPPORTED_SHAPE;
-    if (dtype == MOE_MXFP4 && (d % kMxWord != 0 || I % kMxWord != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (dtype == MOE_MXFP4 && (d % kMxWord != 0 || I % kMxWord != 0 || I > kMxMaxK))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
     // 32-bit row indices and TMA coordinates
     if (static_cast<long long>(max_tokens) * k >= (1LL << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (static_cast<long long>(E) * 2 * I >= (1LL << 30) ||

@@ -9,6 +9,9 @@ namespace moe {
 
 constexpr int kMxBlock = 32;    // values per shared scale
 constexpr int kMxWord = 128;    // values per four scales: the product's K granule
+// The product's largest K: a tile of it takes 16 ms at an SM's share of the HBM's
+// rate, and the item dealer waits for 16 tiles within its second.
+constexpr int kMxMaxK = 1 << 22;
 
 struct MxMatmulParams {
     const uint8_t *a, *as;      // [rows][K/2], [rows][K/32]

@@ -1058,7 +1058,7 @@ extern "C" int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales,
     if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (rows < 0 || (silu_mul != 0 && silu_mul != 1)) return MOE_ERR_INVALID_ARG;
     if (!offsets && n_experts != 1) return MOE_ERR_INVALID_ARG;
-    if (K <= 0 || K % kMxWord != 0 || N <= 0 || N % (silu_mul ? 32 : 16) != 0)
+    if (K <= 0 || K > kMxMaxK || K % kMxWord != 0 || N <= 0 || N % (silu_mul ? 32 : 16) != 0)
         return MOE_ERR_UNSUPPORTED_SHAPE;
     if (n_experts < 1 || n_experts > kMaxExperts) return MOE_ERR_UNSUPPORTED_SHAPE;
     // 32-bit row indices and TMA coordinates

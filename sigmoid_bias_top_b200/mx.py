@@ -175,8 +175,8 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
     [E + 1] (int32, on the device): rows offsets[e] .. offsets[e + 1] - 1 take
     matrix e; rows of no expert are left as they were (as allocated, without
     out). silu_mul: w holds the gate rows, then the up rows, and the result is
-    silu(gate) * up, [rows, N / 2]. K % 128 == 0, N % 16 == 0 (32 with
-    silu_mul), E <= 256. Sums are fp32, rounded once to dtype (bf16 or f32)."""
+    silu(gate) * up, [rows, N / 2]. K % 128 == 0, K <= 2^22, N % 16 == 0
+    (32 with silu_mul), E <= 256. Sums are fp32, rounded once to dtype (bf16 or f32)."""
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("dtype must be float32 or bfloat16")
