@@ -70,6 +70,16 @@ int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t
  * met: MOE_OK or MOE_ERR_DEVICE_TIMEOUT (out of that call is then incomplete). */
 int moe_mx_status(void);
 
+/* For tests of the time-out: moe_mx_matmul with waits of at most timeout_us (1 to
+ * 1000000) whose barriers of one kind (withheld: 1 to 10, 0 for none) wait for an
+ * arrival that nothing makes. Where the call's size has that kind waited for, it
+ * returns within a few times timeout_us plus 40 ms, moe_mx_status tells of it, and
+ * out is unspecified; calls after it are not affected. */
+int moe_mx_selftest_timeout(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                            const uint8_t *w_scales, const int32_t *offsets, int rows, int K,
+                            int n_experts, int N, int silu_mul, void *out, int dtype, int timeout_us,
+                            int withheld, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

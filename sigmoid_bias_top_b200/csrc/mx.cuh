@@ -20,7 +20,13 @@ struct MxMatmulParams {
     void *out;                  // [rows][N], or [rows][N/2] with silu_mul
     int *status;
     int rows, K, E, N, silu_mul, dtype;
+    int wait_us;                // a wait's limit (0: a second)
+    int withheld;               // a kind of barrier that never completes, for the self-test
 };
+
+// The product's kinds of barriers (moe_mx_selftest_timeout).
+enum { kMxFullA = 1, kMxScaledA, kMxEmptyA, kMxFullB, kMxScaledB, kMxEmptyB, kMxTFull, kMxTEmpty,
+       kMxDealt, kMxTaken };
 
 int launch_mx_quantize(const void *x, int dtype, int64_t rows, int K, int64_t ld, uint8_t *codes,
                        uint8_t *scales, cudaStream_t s);

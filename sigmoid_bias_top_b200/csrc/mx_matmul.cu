@@ -32,8 +32,10 @@
 // 6..13 drain the accumulators (two in TMEM, so that a tile's epilogue runs under
 // the next tile's MMAs), warp 14 works out the items (expert, weight tile, row
 // tile), 16 at a time, one a lane: divisions and searches that would cost every
-// other role 2000 cycles per item. All waits are bounded (1 s) and report a
-// time-out in the status word; the kernel then drains its copies and MMAs, frees
+// other role 2000 cycles per item. All waits are bounded (1 s). One that runs out
+// reports it in the status word and tells every role of the CTA, or of both, whose
+// waits then end as well (a warp's for all of its lanes at once, since what follows
+// in it are warp-wide instructions); the kernel drains its copies and MMAs, frees
 // TMEM and returns.
 //
 // What bounds it. Few rows: the weights' stream from HBM; 128 rows of 64 experts,
@@ -70,10 +72,13 @@ constexpr int kMaxStages = 4;
 constexpr int NA = 4;                 // weight stages
 constexpr int A_SLOT = A_BYTES + WM * 16;  // codes and scales
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint64_t kDrainNs = 20000000ull;  // after a time-out, for copies in flight: over a
+                                            // thousand times what one takes
 constexpr uint32_t kPeerBitMask = 0xFEFFFFFFu;  // shared::cluster address in the pair's even CTA
 
 struct MxKernelParams : MxMatmulParams {
     bool sf_tma;                  // the scales come by TMA
+    uint64_t wait_ns;             // a wait's limit
 };
 
 // NT: rows of a tile at most. kPair: a tile is shared by two CTAs.
@@ -115,7 +120,9 @@ struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
     uint64_t dealt[2];            // a set of kDeal items is in place
     uint64_t taken[2];            // every role has read the set
     uint64_t drain;
+    uint64_t wait_ns;
     uint32_t tmem_base;
+    uint32_t peer_abort;          // cluster address of the pair's other abort word (0: none)
     int abort;
 };
 
@@ -137,27 +144,38 @@ __device__ __forceinline__ bool aborted(Ctl *ctl) {
     return *reinterpret_cast<volatile int *>(&ctl->abort) != 0;
 }
 
+// kWarp: the whole warp waits, and all of its lanes get one answer.
+template <bool kWarp>
 __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, Ctl *ctl, int *status) {
-    const uint64_t deadline = globaltimer_ns() + kWaitNs;
+    const uint64_t deadline = globaltimer_ns() + ctl->wait_ns;
     for (uint32_t i = 0;; ++i) {
-        if (try_bar(bar, parity)) return true;
-        if ((i & 255u) == 255u) {
-            if (aborted(ctl)) return false;
-            if (globaltimer_ns() > deadline) break;
+        const bool ok = try_bar(bar, parity);
+        if (kWarp ? __all_sync(0xffffffffu, ok) : ok) return true;
+        if ((i & 15u) == 15u) {
+            bool stop = aborted(ctl);
+            if (!stop && globaltimer_ns() > deadline) {
+                stop = true;
+                set_status(status, kStatusTimeout);
+                atomicExch(&ctl->abort, 1);
+                if (ctl->peer_abort != 0u)  // it cannot exit before this CTA
+                    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(ctl->peer_abort)
+                                 : "memory");
+            }
+            if (kWarp ? __any_sync(0xffffffffu, stop) : stop) return false;
         }
     }
-    set_status(status, kStatusTimeout);
-    atomicExch(&ctl->abort, 1);
-    return false;
 }
 
+template <bool kWarp>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, Ctl *ctl, int *status) {
     // a try suspends the thread for a while by itself; a few of them cover any
     // wait of a running pipeline
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (try_bar(bar, parity)) return true;
-    return wait_bar_slow(bar, parity, ctl, status);
+    for (int i = 0; i < 64; ++i) {
+        const bool ok = try_bar(bar, parity);
+        if (kWarp ? __all_sync(0xffffffffu, ok) : ok) return true;
+    }
+    return wait_bar_slow<kWarp>(bar, parity, ctl, status);
 }
 
 __device__ __forceinline__ void arrive_bar(uint32_t bar) {
@@ -373,7 +391,7 @@ struct Walk {
     // false at the end of the list, or after a time-out
     __device__ __forceinline__ bool next(Item &it) {
         const int set = (i / kDeal) & 1;
-        if (i % kDeal == 0 && !wait_bar(MX_BAR(dealt, set), (i / (2 * kDeal)) & 1u, ctl, status)) return false;
+        if (i % kDeal == 0 && !wait_bar<kWarp>(MX_BAR(dealt, set), (i / (2 * kDeal)) & 1u, ctl, status)) return false;
         const uint4 v = ld_shared(bars + static_cast<uint32_t>(sizeof(Ctl)) +
                                   (set * kDeal + i % kDeal) * static_cast<uint32_t>(sizeof(int4)));
         it.wrow = static_cast<int>(v.x);
@@ -454,8 +472,8 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
             uint4 a[4], b[4 * C::NB];
             const bool load_a = !kPair || it.first;
             if (p.sf_tma) {
-                if (kPair && it.first && !wait_bar(MX_BAR(scaleda, as), aph, ctl, p.status)) return;
-                if (!wait_bar(MX_BAR(scaledb, s), ph, ctl, p.status)) return;
+                if (kPair && it.first && !wait_bar<true>(MX_BAR(scaleda, as), aph, ctl, p.status)) return;
+                if (!wait_bar<true>(MX_BAR(scaledb, s), ph, ctl, p.status)) return;
                 const uint32_t sfa = smem + as * A_SLOT + A_BYTES + lane * 16;
                 const uint32_t sfb = smem + NA * A_SLOT + s * C::B_SLOT + C::B_BYTES + lane * 16;
                 if (load_a) {
@@ -466,7 +484,7 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
                 for (int i = 0; i < 4 * C::NB; ++i) b[i] = i < C::R ? ld_shared(sfb + i * 512) : b[0];
             } else {
                 if (load_a) {
-                    if (kPair && !wait_bar(MX_BAR(emptya, as), aph ^ 1u, ctl, p.status)) return;
+                    if (kPair && !wait_bar<true>(MX_BAR(emptya, as), aph ^ 1u, ctl, p.status)) return;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         // gate/up: 16 gate rows and their 16 up rows in turn
@@ -485,7 +503,7 @@ __device__ __forceinline__ void bring_scales(const MxKernelParams &p, Ctl *ctl, 
             if (warmup > 0) {
                 --warmup;
             } else {
-                if (!wait_bar(MX_BAR(emptyb, os), oph, ctl, p.status)) return;
+                if (!wait_bar<true>(MX_BAR(emptyb, os), oph, ctl, p.status)) return;
                 if (++os == C::STAGES) { os = 0; oph ^= 1u; }
             }
             tc_fence_after();
@@ -642,26 +660,34 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     const bool leader = half == 0;
 
     if (threadIdx.x == 0) {
+        // one kind of barrier may wait for an arrival that nothing makes (p.withheld)
+        auto init = [&](uint64_t *bar, int count, int kind) { mbar_init(bar, count + (p.withheld == kind)); };
         for (int s = 0; s < C::STAGES; ++s) {
             // the rows' TMA thread (of the leader; both of a single CTA), the scale
             // warps (of both CTAs)
-            mbar_init(&ctl->fullb[s], (kPair ? 1 : 2) + kCtas * kScaleWarps);
-            mbar_init(&ctl->scaledb[s], kPair ? 1 : 2);
-            mbar_init(&ctl->emptyb[s], 1);
+            init(&ctl->fullb[s], (kPair ? 1 : 2) + kCtas * kScaleWarps, kMxFullB);
+            init(&ctl->scaledb[s], kPair ? 1 : 2, kMxScaledB);
+            init(&ctl->emptyb[s], 1, kMxEmptyB);
         }
         for (int s = 0; s < NA; ++s) {
-            mbar_init(&ctl->fulla[s], 1);  // the weights' TMA thread (of the leader)
-            mbar_init(&ctl->scaleda[s], 1);
-            mbar_init(&ctl->emptya[s], 1);
+            init(&ctl->fulla[s], 1, kMxFullA);  // the weights' TMA thread (of the leader)
+            init(&ctl->scaleda[s], 1, kMxScaledA);
+            init(&ctl->emptya[s], 1, kMxEmptyA);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl->tfull[b], 1);
-            mbar_init(&ctl->tempty[b], kCtas * kEpiWarps);
-            mbar_init(&ctl->dealt[b], 1);
+            init(&ctl->tfull[b], 1, kMxTFull);
+            init(&ctl->tempty[b], kCtas * kEpiWarps, kMxTEmpty);
+            init(&ctl->dealt[b], 1, kMxDealt);
             // every role but the dealer; one CTA of a pair has no MMA thread
-            mbar_init(&ctl->taken[b], 2 + kScaleWarps + kEpiWarps + (leader ? 1 : 0));
+            init(&ctl->taken[b], 2 + kScaleWarps + kEpiWarps + (leader ? 1 : 0), kMxTaken);
         }
         mbar_init(&ctl->drain, 1);
+        ctl->wait_ns = p.wait_ns;
+        ctl->peer_abort = 0;
+        if constexpr (kPair)
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(ctl->peer_abort)
+                         : "r"(smem_u32(&ctl->abort)), "r"(half ^ 1));
         ctl->abort = 0;
         fence_mbar_init();
     }
@@ -748,7 +774,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 const int wrow = it.wrow + half * kCtaOutputs;
                 const int trow = it.t0 + half * (mma_n<C>(it) / 2);
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!wait_bar(kPair && weights ? MX_BAR(emptya, s) : MX_BAR(emptyb, s), ph ^ 1u, ctl, p.status)) {
+                    if (!wait_bar<false>(kPair && weights ? MX_BAR(emptya, s) : MX_BAR(emptyb, s), ph ^ 1u, ctl, p.status)) {
                         ok = false;
                         break;
                     }
@@ -787,9 +813,8 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 }
             }
             // (a pair's copies complete on the leader's barriers)
-            if (!ok || aborted(ctl)) {  // let the other roles leave and our own copies land
-                atomicExch(&ctl->abort, 1);
-                const uint64_t dl = globaltimer_ns() + kWaitNs;
+            if (!ok || aborted(ctl)) {  // our own copies land
+                const uint64_t dl = globaltimer_ns() + kDrainNs;
                 for (int i = 0; i < stages; ++i)
                     if (issued[i]) {
                         const bool a = kPair && weights;
@@ -811,7 +836,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             for (; walk.next(it); ++tile) {
                 const int buf = tile & 1;
                 const uint32_t use = static_cast<uint32_t>(tile >> 1);
-                if (!wait_bar(MX_BAR(tempty, buf), (use & 1u) ^ 1u, ctl, p.status)) break;
+                if (!wait_bar<false>(MX_BAR(tempty, buf), (use & 1u) ^ 1u, ctl, p.status)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * NT);
                 const int n = mma_n<C>(it);
@@ -820,8 +845,8 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
                 int as = run_as;
                 uint32_t aph = run_aph;
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (kPair && it.first && !wait_bar(MX_BAR(fulla, as), aph, ctl, p.status)) { ok = false; break; }
-                    if (!wait_bar(MX_BAR(fullb, s), ph, ctl, p.status)) { ok = false; break; }
+                    if (kPair && it.first && !wait_bar<false>(MX_BAR(fulla, as), aph, ctl, p.status)) { ok = false; break; }
+                    if (!wait_bar<false>(MX_BAR(fullb, s), ph, ctl, p.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a0 = desc0 + static_cast<uint32_t>(as) * (A_SLOT / 16);
                     const uint32_t b0 = desc0 + (NA * A_SLOT + static_cast<uint32_t>(s) * C::B_SLOT) / 16;
@@ -857,7 +882,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     } else if (warp == kThreads / 32 - 2) {
         // ------------------------- item dealer --------------------------
         for (int c = 0;; ++c) {
-            if (c >= 2 && !wait_bar(MX_BAR(taken, c & 1), ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
+            if (c >= 2 && !wait_bar<true>(MX_BAR(taken, c & 1), ((c >> 1) & 1u) ^ 1u, ctl, p.status)) break;
             const int64_t item = begin + (static_cast<int64_t>(c) * kDeal + lane) * (kPair ? 1 : crew);
             int4 it = make_int4(0, 0, 0, 0);
             if (lane < kDeal && item < end)
@@ -865,7 +890,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
             if (lane < kDeal) items[(c & 1) * kDeal + lane] = it;
             __syncwarp();
             if (lane == 0) arrive_bar(MX_BAR(dealt, c & 1));
-            if (__any_sync(0xffffffffu, lane < kDeal && it.w == 0) || aborted(ctl)) break;
+            if (__any_sync(0xffffffffu, (lane < kDeal && it.w == 0) || aborted(ctl))) break;
         }
     } else {
         // --------------------------- epilogue ---------------------------
@@ -880,7 +905,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
         for (; walk.next(it); ++tile) {
             const int buf = tile & 1;
             const uint32_t use = static_cast<uint32_t>(tile >> 1);
-            if (!wait_bar(MX_BAR(tfull, buf), use & 1u, ctl, p.status)) break;
+            if (!wait_bar<true>(MX_BAR(tfull, buf), use & 1u, ctl, p.status)) break;
             tc_fence_after();
             const uint32_t t_lane = tmem_base + static_cast<uint32_t>(buf * NT) +
                                     (static_cast<uint32_t>(q * 32) << 16);
@@ -905,6 +930,13 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
     if (warp == 1) {
         __syncwarp();
         X::dealloc(tmem_base, C::TMEM_COLS);
+    }
+    // After a time-out a stage's barrier may lack other roles' arrivals, or be in the
+    // pair's other CTA, and not tell of a copy; nothing issues any more, and the CTA
+    // stays until all have had the time to land.
+    if (threadIdx.x == 0 && aborted(ctl)) {
+        const uint64_t dl = globaltimer_ns() + kDrainNs;
+        while (globaltimer_ns() < dl) __nanosleep(1000);
     }
 }
 
@@ -982,6 +1014,7 @@ int launch(const MxMatmulParams &args, int n_sm, cudaStream_t s) {
     CUtensorMap w, a, sw = {}, sa = {};
     MxKernelParams p;
     static_cast<MxMatmulParams &>(p) = args;
+    p.wait_ns = args.wait_us > 0 ? static_cast<uint64_t>(args.wait_us) * 1000u : kWaitNs;
     // TMA wants 16-byte row pitches and addresses
     p.sf_tma = p.K % BK == 0 && aligned(p.ws, 16) && aligned(p.as, 16);
     int rc;
@@ -1051,10 +1084,9 @@ int launch_mx_matmul(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
 
 using namespace moe;
 
-extern "C" int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales,
-                             const uint8_t *w_codes, const uint8_t *w_scales,
-                             const int32_t *offsets, int rows, int K, int n_experts, int N,
-                             int silu_mul, void *out, int dtype, void *stream) {
+static int matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                  const uint8_t *w_scales, const int32_t *offsets, int rows, int K, int n_experts,
+                  int N, int silu_mul, void *out, int dtype, int wait_us, int withheld, void *stream) {
     if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
     if (rows < 0 || (silu_mul != 0 && silu_mul != 1)) return MOE_ERR_INVALID_ARG;
     if (!offsets && n_experts != 1) return MOE_ERR_INVALID_ARG;
@@ -1072,13 +1104,32 @@ extern "C" int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales,
     MxMatmulParams p = {};
     p.a = a_codes; p.as = a_scales; p.w = w_codes; p.ws = w_scales; p.offsets = offsets;
     p.out = out; p.rows = rows; p.K = K; p.E = n_experts; p.N = N; p.silu_mul = silu_mul;
-    p.dtype = dtype;
+    p.dtype = dtype; p.wait_us = wait_us; p.withheld = withheld;
     int dev = 0, n_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return MOE_ERR_NO_DEVICE;
     if (status_address(&p.status) != MOE_OK) return MOE_ERR_CUDA;
     return launch_mx_matmul(p, n_sm, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales,
+                             const uint8_t *w_codes, const uint8_t *w_scales,
+                             const int32_t *offsets, int rows, int K, int n_experts, int N,
+                             int silu_mul, void *out, int dtype, void *stream) {
+    return matmul(a_codes, a_scales, w_codes, w_scales, offsets, rows, K, n_experts, N, silu_mul, out,
+                  dtype, 0, 0, stream);
+}
+
+extern "C" int moe_mx_selftest_timeout(const uint8_t *a_codes, const uint8_t *a_scales,
+                                       const uint8_t *w_codes, const uint8_t *w_scales,
+                                       const int32_t *offsets, int rows, int K, int n_experts,
+                                       int N, int silu_mul, void *out, int dtype, int timeout_us,
+                                       int withheld, void *stream) {
+    if (timeout_us <= 0 || timeout_us > 1000000 || withheld < 0 || withheld > kMxTaken)
+        return MOE_ERR_INVALID_ARG;
+    return matmul(a_codes, a_scales, w_codes, w_scales, offsets, rows, K, n_experts, N, silu_mul, out,
+                  dtype, timeout_us, withheld, stream);
 }
 
 extern "C" int moe_mx_status(void) {

@@ -42,9 +42,10 @@ def lib():
         L.moe_mx_quantize.argtypes = [P, I, I64, I, I64, P, P, P]
         L.moe_mx_dequantize.argtypes = [P, P, I64, I, P, I, P]
         L.moe_mx_matmul.argtypes = [P, P, P, P, P, I, I, I, I, I, P, I, P]
+        L.moe_mx_selftest_timeout.argtypes = [P, P, P, P, P, I, I, I, I, I, P, I, I, I, P]
         L.moe_mx_status.argtypes = []
         for f in (L.moe_mx_quantize, L.moe_mx_dequantize, L.moe_mx_matmul,
-                  L.moe_mx_status):
+                  L.moe_mx_selftest_timeout, L.moe_mx_status):
             f.restype = I
         _bound = True
     return L

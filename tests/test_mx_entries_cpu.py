@@ -28,3 +28,12 @@ def test_layer_width():
     assert create(1 << 22) == -1
     assert create((1 << 22) + 128) == -2 and create(1 << 28) == -2
     assert create((1 << 22) + 128, sb.MOE_FP8_BLOCK) == -1     # other layers as they were
+
+
+def test_selftest_timeout_refusals():
+    def call(timeout_us=1000, withheld=1, rows=4, K=256, out=256):
+        return mx.lib().moe_mx_selftest_timeout(256, 256, 256, 256, 256, rows, K, 2, 64, 0, out, 1,
+                                                timeout_us, withheld, None)
+    assert call(timeout_us=0) == -1 and call(timeout_us=1000001) == -1
+    assert call(withheld=-1) == -1 and call(withheld=11) == -1
+    assert call(out=None) == -1 and call(K=64) == -2
