@@ -58,15 +58,20 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device, without buildin
 class _On:
     """Makes the device of the tensors and the stream to launch on current (the
     given stream, or that device's current one), so that copies and outputs made
-    inside belong to that stream too. Only needed where _here says no."""
+    inside belong to that stream too. Only needed where _here says no. A stream that
+    was given is recorded as a user of the tensors: the memory of those dropped
+    after the call is not handed out again before the stream is done with them."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *tensors):
         if stream is None:
             self.inner = torch.cuda.device(device)
         else:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
             self.inner = torch.cuda.stream(stream)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
     def __enter__(self):
         self.inner.__enter__()
@@ -120,7 +125,7 @@ def quantize(x: torch.Tensor, out: Optional[MxTensor] = None, stream=None) -> Mx
         raise ValueError(f"x must have rows of fewer than 2^31 values, got {shape[-1]}")
     device = x.device
     if not _here(device, stream):
-        with _On(device, stream):
+        with _On(device, stream, x, *(out or ())):
             return quantize(x, out)
     K = ld = shape[-1]
     if not x.is_contiguous():
@@ -156,7 +161,7 @@ def dequantize(q: MxTensor, dtype=torch.bfloat16, out=None, stream=None) -> torc
     if K == 0:
         raise ValueError("q has no columns")
     if not _here(device, stream):
-        with _On(device, stream):
+        with _On(device, stream, codes, scales, out):
             return dequantize(q, dtype, out)
     if out is None:
         out = codes.new_empty((*shape[:-1], K), dtype=dtype)
@@ -197,7 +202,7 @@ def matmul(a: MxTensor, w: MxTensor, offsets: Optional[torch.Tensor] = None,
             raise ValueError(f"offsets must be a contiguous int32 ({E + 1},) tensor on {device}")
         offs = offsets.data_ptr()
     if not _here(device, stream):
-        with _On(device, stream):
+        with _On(device, stream, ac, as_, wc, ws, offsets, out):
             return matmul(a, w, offsets, silu_mul, dtype, out)
     if out is None:
         out = ac.new_empty((rows, N // 2 if silu_mul else N), dtype=dtype)
