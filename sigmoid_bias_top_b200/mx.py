@@ -51,8 +51,11 @@ def lib():
     return L
 
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device, without building a Stream
+# The current device, and the current stream's handle on a device without building a
+# Stream; the public functions where torch has no such ones.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 class _On:
