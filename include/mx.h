@@ -66,8 +66,10 @@ int moe_mx_matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t
                   int N, int silu_mul, void *out, int dtype, void *stream);
 
 /* moe_mx_matmul waits inside its kernel with a limit of a second. Waits for the
- * device, then reads and clears what the calls on it since the last reading
- * met: MOE_OK or MOE_ERR_DEVICE_TIMEOUT (out of that call is then incomplete). */
+ * current device, then tells what the calls on it, of any thread, met since the
+ * calling thread's last reading (its first: since the program's start): MOE_OK or
+ * MOE_ERR_DEVICE_TIMEOUT (out of a call is then incomplete). A reading leaves what
+ * other threads will be told as it is. */
 int moe_mx_status(void);
 
 /* For tests of the time-out: moe_mx_matmul with waits of at most timeout_us (1 to

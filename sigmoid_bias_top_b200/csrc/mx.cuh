@@ -18,8 +18,9 @@ struct MxMatmulParams {
     const uint8_t *w, *ws;      // [E][N][K/2], [E][N][K/32]
     const int32_t *offsets;     // [E+1], or null: one group of all rows
     void *out;                  // [rows][N], or [rows][N/2] with silu_mul
-    int *status;
+    int *status;                // a context's status word, or (counts) a count of time-outs
     int rows, K, E, N, silu_mul, dtype;
+    int counts;                 // waits that run out are counted in *status
     int wait_us;                // a wait's limit (0: a second)
     int withheld;               // a kind of barrier that never completes, for the self-test
 };

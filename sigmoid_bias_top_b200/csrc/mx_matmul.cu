@@ -49,6 +49,8 @@
 #include <cooperative_groups.h>
 #include <stddef.h>
 
+#include <map>
+
 #include "mx.cuh"
 
 namespace cg = cooperative_groups;
@@ -123,6 +125,7 @@ struct __align__(16) Ctl {  // the items behind it are read 16 bytes at a time
     uint64_t wait_ns;
     uint32_t tmem_base;
     uint32_t peer_abort;          // cluster address of the pair's other abort word (0: none)
+    int counts;                   // the status word counts time-outs
     int abort;
 };
 
@@ -155,7 +158,8 @@ __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, Ctl *c
             bool stop = aborted(ctl);
             if (!stop && globaltimer_ns() > deadline) {
                 stop = true;
-                set_status(status, kStatusTimeout);
+                if (ctl->counts) atomicAdd(status, 1);
+                else set_status(status, kStatusTimeout);
                 atomicExch(&ctl->abort, 1);
                 if (ctl->peer_abort != 0u)  // it cannot exit before this CTA
                     asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(ctl->peer_abort)
@@ -701,6 +705,7 @@ __device__ __forceinline__ void mx_matmul_body(const CUtensorMap &tmW, const CUt
         }
         mbar_init(&ctl->drain, 1);
         ctl->wait_ns = p.wait_ns;
+        ctl->counts = p.counts;
         ctl->peer_abort = 0;
         if constexpr (kPair)
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -975,8 +980,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx_matmul_body<NT, true, kSilu, T>(tmW, tmA, tmSW, tmSA, p);
 }
 
-// Device-side failures of calls without a context (moe_mx_status).
-__device__ int g_mx_status;
+// Waits that ran out in calls without a context (moe_mx_status). Only counted up, so
+// that one thread's reading takes nothing from another's.
+__device__ int g_mx_timeouts;
 
 // CTA pairs that can be resident at once (an SM without a partner in its GPC
 // cannot host half a pair), at most one pair per two SMs.
@@ -1076,9 +1082,10 @@ int launch_nt(const MxMatmulParams &p, int n_sm, cudaStream_t s) {
                       : launch<NT, kPair, false, __nv_bfloat16>(p, n_sm, s);
 }
 
-int status_address(int **out) {
-    return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_mx_status) == cudaSuccess ? MOE_OK
-                                                                                       : MOE_ERR_CUDA;
+int timeouts_address(int **out) {
+    return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_mx_timeouts) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -1127,7 +1134,8 @@ static int matmul(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return MOE_ERR_NO_DEVICE;
-    if (status_address(&p.status) != MOE_OK) return MOE_ERR_CUDA;
+    p.counts = 1;
+    if (timeouts_address(&p.status) != MOE_OK) return MOE_ERR_CUDA;
     return launch_mx_matmul(p, n_sm, static_cast<cudaStream_t>(stream));
 }
 
@@ -1151,10 +1159,14 @@ extern "C" int moe_mx_selftest_timeout(const uint8_t *a_codes, const uint8_t *a_
 }
 
 extern "C" int moe_mx_status(void) {
-    int *status = nullptr, v = 0;
-    if (status_address(&status) != MOE_OK || cudaDeviceSynchronize() != cudaSuccess ||
-        cudaMemcpy(&v, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(status, 0, sizeof(int)) != cudaSuccess)
+    static thread_local std::map<int, int> seen;  // by device
+    int *timeouts = nullptr, v = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || timeouts_address(&timeouts) != MOE_OK ||
+        cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(&v, timeouts, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return v & kStatusTimeout ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
+    int &before = seen[dev];
+    const bool more = v != before;
+    before = v;
+    return more ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }

@@ -230,7 +230,8 @@ def quantize_experts(layer):
 
 
 def status(device=None) -> int:
-    """Waits for the device; 0, or the code of a time-out inside a matmul on it
-    since the last call (whose result is then incomplete)."""
+    """Waits for the device; 0, or the code of a time-out inside a matmul on it, by any
+    thread, since this thread's last call (the result is then incomplete). Every
+    thread that asks is told."""
     with torch.cuda.device(device):
         return lib().moe_mx_status()

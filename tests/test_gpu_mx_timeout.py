@@ -84,3 +84,19 @@ def test_a_layer_reports_its_own():
     assert torch.equal(m(x), want) and m.status() == 0
     assert mx.status() == TIMEOUT and mx.status() == 0
     m.close()
+
+
+def test_every_thread_is_told():
+    """One thread's reading does not take a time-out from another's."""
+    from concurrent.futures import ThreadPoolExecutor
+    a, w, off = make(17, 256, 128, 1)
+    with ThreadPoolExecutor(1) as other:
+        def status():
+            return other.submit(mx.status, "cuda:0").result()
+        status(), mx.status()
+        run(a, w, off, FULL_B)
+        assert status() == TIMEOUT and mx.status() == TIMEOUT
+        assert status() == 0 and mx.status() == 0
+        run(a, w, off, FULL_B)
+        assert mx.status() == TIMEOUT and status() == TIMEOUT
+        assert mx.status() == 0 and status() == 0
