@@ -36,6 +36,8 @@
 // in flight (again bounded), frees TMEM and returns.
 #include <dlfcn.h>
 
+#include <atomic>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -343,14 +345,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn get_encoder() {
-    static EncodeTiledFn fn = nullptr;
+    static std::atomic<EncodeTiledFn> found{nullptr};  // any thread may be the first
+    EncodeTiledFn fn = found.load(std::memory_order_relaxed);
     if (!fn) {
         void *ptr = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+            found.store(fn = reinterpret_cast<EncodeTiledFn>(ptr), std::memory_order_relaxed);
     }
     return fn;
 }

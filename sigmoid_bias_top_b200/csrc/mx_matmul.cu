@@ -49,6 +49,7 @@
 #include <cooperative_groups.h>
 #include <stddef.h>
 
+#include <atomic>
 #include <map>
 
 #include "mx.cuh"
@@ -1009,14 +1010,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 // rows up_offset further each (as tc_encode_pair_4d has it for the codes).
 int encode_scales(CUtensorMap *m, const void *base, uint64_t rows, uint64_t pitch, uint32_t box_rows,
                   uint64_t up_offset) {
-    static void *fn = nullptr;
+    static std::atomic<void *> found{nullptr};  // any thread may be the first
+    void *fn = found.load(std::memory_order_relaxed);
     if (!fn) {
         cudaDriverEntryPointQueryResult q;
         void *ptr = nullptr;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
             q != cudaDriverEntryPointSuccess || !ptr)
             return MOE_ERR_CUDA;
-        fn = ptr;
+        found.store(fn = ptr, std::memory_order_relaxed);
     }
     const bool paired = up_offset != 0;
     const cuuint64_t dims[4] = {pitch / 2, paired ? 16 : rows, 2, paired ? (rows - up_offset) / 16 : 0};
@@ -1061,8 +1063,8 @@ int launch(const MxMatmulParams &args, int n_sm, cudaStream_t s) {
     if constexpr (kPair) {
         auto kern = mx_matmul_pair_kernel<NT, kSilu, T>;
         if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
-        static int resident = 0;  // per kernel, for the device model of the process
-        if (resident == 0) resident = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
+        // per kernel, for the device model of the process; any thread may be the first
+        static const int resident = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
         const int pairs = static_cast<int>(items < resident ? items : resident);
         return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, w, a, sw, sa, p);
     } else {
