@@ -815,8 +815,8 @@ int launch(const PairMaps &m, const Fp8PairParams &p, int n_sm, cudaStream_t s) 
     auto kern = fp8_pair_kernel<GATE_UP>;
     const size_t smem = smem_bytes(p.E);
     if (ensure_smem(kern, smem) != MOE_OK) return MOE_ERR_CUDA;
-    // per kernel, for the device model of the process; any thread may be the first
-    static const int pairs = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
+    static int pairs = 0;  // per kernel, for the device model of the process
+    if (pairs == 0) pairs = resident_pairs(reinterpret_cast<const void *>(kern), smem, n_sm);
     return launch_k(kern, dim3(2 * pairs), dim3(kThreads), smem, s, m, p);
 }
 
