@@ -414,30 +414,27 @@ struct Walk {
     }
 };
 
-// silu(g) * u, silu(g) = g / (1 + exp(-g)) down to fp32's last subnormal number (u
-// may be large): exp(-g) itself is infinite from -88.7 on, and the fast division
-// gives 0 for divisors above 2^126.
-// For a bf16 result both sides of the division are scaled by 2^-32: exp(-g) 2^-32
-// stays under 2^126 down to -109, where silu is 2^-150. The divisor is never a
-// subnormal number, nor its reciprocal where that matters, so the instructions that
-// flush them serve (and no others around them). The exponential's argument is rounded
-// to half an ulp of 32 and more, 2^-19 to 2^-16 relative (and 2^-21 for the rest),
-// which leaves the result's rounding alone.
-// For fp32 the exponential is that of -|g| / 2 and squared, the division a full one,
-// and a negative gate's factor exp(g) is taken half with g and half with u: 2^-20
-// relative and |g| 2^-23. (As the bf16 form it cost gate/up prefill 5%.)
-template <bool kFast>
+// silu(g) * u = g / (1 + exp(-g)) * u. exp(-g) is infinite from -88.7 on, and 1 over
+// it a subnormal number before, while u may be large: a negative gate's factor exp(g),
+// as the square of exp(g / 2), is taken half with g and half with u, so that it
+// underflows only where the result does. 2^-20 relative and |g| 2^-23.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    if constexpr (kFast) {
-        float e, r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(g, -1.44269504f, -32.0f)));  // log2(e)
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(0x1p-32f + e));
-        return g * 0x1p-32f * r * u;
-    } else {
-        const float h = expf(-0.5f * fabsf(g));
-        const float f = g < 0.f ? h : 1.0f;
-        return g * f / (1.0f + h * h) * (u * f);
-    }
+    const float h = expf(-0.5f * fabsf(g));
+    const float f = g < 0.f ? h : 1.0f;
+    return g * f / (1.0f + h * h) * (u * f);
+}
+
+// The same for a bf16 result and gates not below kFarGate: the divisor is at most
+// 2^116, so the exponential and the reciprocal may be the fast ones that flush
+// subnormal numbers. 2^-20 relative and |g| 2^-23 from the rounded product with
+// log2(e), 2^-16 at most, which leaves the result's rounding alone. (The form above
+// for every gate cost gate/up prefill 5%.)
+constexpr float kFarGate = -80.f;
+__device__ __forceinline__ float silu_mul_near(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));  // log2(e)
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 // 32 TMEM lanes x 4 R columns: column 4 j + i of row group count R, i.e. word j
@@ -609,10 +606,26 @@ struct Drain {
         tmem_ld_wait(lo);
         tmem_ld_wait(hi);
         if constexpr (kSilu) {
+            // which form a value takes depends on its own gate alone; the branch only
+            // saves the second form where no value of the thread needs it
+            float least = 0.f;
+            if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                lo[i] = __float_as_uint(
-                    silu_mul<sizeof(T) == 2>(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
+                for (int i = 0; i < 16; ++i) least = fminf(least, __uint_as_float(lo[i]));
+            }
+            if (sizeof(T) == 2 && least >= kFarGate) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    lo[i] = __float_as_uint(silu_mul_near(__uint_as_float(lo[i]), __uint_as_float(hi[i])));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float g = __uint_as_float(lo[i]), u = __uint_as_float(hi[i]);
+                    lo[i] = __float_as_uint(sizeof(T) == 2 && !(g < kFarGate) ? silu_mul_near(g, u)
+                                                                              : silu_mul(g, u));
+                }
+            }
+            __syncwarp();  // the stores below are the whole warp's
         }
         if constexpr (sizeof(T) == 2) {
             // fragment registers 4g, 4g + 1 are rows 8g.. of outputs 0..7, 4g + 2

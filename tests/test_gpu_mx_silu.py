@@ -2,14 +2,10 @@
 is large, so that the result is an ordinary number.
 
 Gates and ups are sums of a few MXFP4 values that fp32 holds exactly, so only
-the activation rounds. For bf16 the argument of the exponential, up to 256 as a
-power of 2, is off by 2^-16 from the rounded log2(e) and the rounded product, so
-the exponential by 2^-16 and, with the division, 2^-21. For fp32 it is 2^-21 and
-|gate| 2^-23 for the exponential, 2^-22 for the division and 2^-21 for the other
-roundings. silu(gate) is an fp32 number, off by a step of its subnormal ones
-(2^-149), times up. The result is rounded once; below its type's normal numbers it
-is off by half a step of those (2^-134 for bf16, 2^-150 for fp32) and by one of
-fp32's."""
+the activation rounds: its exponential by 2^-21 and, from the rounded product with
+log2(e), |gate| 2^-23; the division (2^-22) and the other roundings by 2^-21
+together. The result is rounded once; below its type's normal numbers it is off by
+half a step of those (2^-134 for bf16, 2^-150 for fp32) and by one of fp32's."""
 import pytest
 import torch
 
@@ -17,6 +13,17 @@ from sigmoid_bias_top_b200 import mx
 from tests import mx_ref as R
 
 pytestmark = pytest.mark.gpu
+
+
+def check(y, g, u, dtype):
+    want = g * torch.sigmoid(g) * u
+    eps = torch.finfo(dtype).eps / 2
+    rel = (g.abs().clamp_max(256) + 8) * 2.0 ** -23      # no exponential left above
+    step = 2.0 ** -134 if dtype is torch.bfloat16 else 2.0 ** -150
+    err = want.abs() * rel
+    bound = err + eps * (want.abs() + err) + step + 2.0 ** -149
+    worst = (y - want).abs() / bound
+    assert worst.max() <= 1, (float(worst.max()), float(g.flatten()[worst.argmax()]))
 
 
 def pieces(v, n=4):
@@ -59,12 +66,26 @@ def test_far_gates(rows, I, K, dtype):
     y = mx.matmul(qa, qw, silu_mul=True, dtype=dtype).double().cpu()
     p = a.double() @ w.double().t()
     g, u = p[:, :I], p[:, I:]
-    want = g * torch.sigmoid(g) * u
-    bf16 = dtype is torch.bfloat16
-    eps = torch.finfo(dtype).eps / 2
-    rel = 2.0 ** -16 + 2.0 ** -21 if bf16 else (g.abs() + 8) * 2.0 ** -23
-    step = 2.0 ** -134 if bf16 else 2.0 ** -150
-    err = want.abs() * rel + u.abs() * 2.0 ** -149
-    bound = err + eps * (want.abs() + err) + step + 2.0 ** -149
-    worst = ((y - want).abs() / bound)
-    assert worst.max() <= 1, (float(worst.max()), float(g.flatten()[worst.argmax()]))
+    check(y, g, u, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,I", [(5, 512), (200, 3264)])
+def test_gates_of_every_magnitude(rows, I, dtype):
+    """Gates of +-2^-125 to 2^119 beside ups that make the results ordinary."""
+    e = torch.arange(I) % 245 - 125                       # of the gates
+    up = (-e).clamp(-100, 120)
+    w = torch.zeros(2 * I, 128)
+    w[:I, 0] = torch.where(torch.arange(I) % 2 == 1, -1.0, 1.0)
+    w[I:, 0] = 1.5
+    q = mx.quantize(w.cuda())
+    shift = torch.cat([e, up]).to(torch.int16)
+    block = q.scales[:, 0].cpu().to(torch.int16) + shift
+    assert block.min() >= 0 and block.max() < 255
+    q.scales[:, 0] = block.to(torch.uint8).cuda()
+    a = torch.zeros(rows, 128)
+    a[:, 0] = 1.0
+    qa = mx.quantize(a.cuda())
+    g = (w[:I, 0].double() * 2.0 ** e.double()).expand(rows, I)
+    u = (w[I:, 0].double() * 2.0 ** up.double()).expand(rows, I)
+    check(mx.matmul(qa, q, silu_mul=True, dtype=dtype).double().cpu(), g, u, dtype)
