@@ -96,7 +96,9 @@ static const char *kMxKernelNames[] = {"route", "dispatch", "quantize", "gate_up
 
 static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int moe::ensure_smem_ptr(const void *kern, size_t smem) {
+// No exception leaves it (the map's first entry of a kernel allocates): its callers
+// are C entries.
+int moe::ensure_smem_ptr(const void *kern, size_t smem) try {
     static std::mutex mu;
     static std::map<std::pair<int, const void *>, size_t> set;  // the limit is a device's own
     if (smem <= 48 * 1024) return MOE_OK;
@@ -115,6 +117,8 @@ int moe::ensure_smem_ptr(const void *kern, size_t smem) {
     }
     cur = smem;
     return MOE_OK;
+} catch (...) {
+    return MOE_ERR_OOM;
 }
 
 extern "C" const char *moe_strerror(int code) {

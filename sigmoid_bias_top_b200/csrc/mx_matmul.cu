@@ -50,7 +50,6 @@
 #include <stddef.h>
 
 #include <atomic>
-#include <map>
 
 #include "mx.cuh"
 
@@ -1174,14 +1173,15 @@ extern "C" int moe_mx_selftest_timeout(const uint8_t *a_codes, const uint8_t *a_
 }
 
 extern "C" int moe_mx_status(void) {
-    static thread_local std::map<int, int> seen;  // by device
+    constexpr int kMaxDevices = 64;
+    static thread_local int seen[kMaxDevices];
     int *timeouts = nullptr, v = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || timeouts_address(&timeouts) != MOE_OK ||
         cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpy(&v, timeouts, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
         return MOE_ERR_CUDA;
-    int &before = seen[dev];
-    const bool more = v != before;
-    before = v;
+    if (dev >= kMaxDevices) return MOE_ERR_NO_DEVICE;
+    const bool more = v != seen[dev];
+    seen[dev] = v;
     return more ? MOE_ERR_DEVICE_TIMEOUT : MOE_OK;
 }
