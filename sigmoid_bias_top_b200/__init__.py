@@ -222,6 +222,9 @@ class MoeLayer:
         self.device = wgu.device
 
     def forward(self, x, out=None, stream=None):
+        """out = the block of x [n, d] (bf16 for FP8_BLOCK and MXFP4 layers). On another
+        stream than the current one, x and out must be kept until its work is done: the
+        allocator is not told of it."""
         import torch
         n = x.shape[0]
         if out is None:

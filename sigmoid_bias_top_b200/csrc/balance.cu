@@ -22,10 +22,11 @@
 // a row at a time from its logits, which are read again: the scores cost less
 // to form than to store and load.
 //
-// 131072 tokens of 256 experts (fp32, 61 sequences): 37 us for the sums (3.7 TB/s;
-// 57 with one row in flight and full-precision exponentials), 8 for the last
-// reduction, 46 for the gradient (5.8 TB/s; 64 likewise). 64 tokens take 17 us on
-// the device, under the 100 that torch's autograd and the calls take on the host.
+// 131072 tokens of 256 experts (fp32, 61 sequences): 44 us for the sums and the last
+// reduction (36 and 8; a lane's two rows in flight are both worked on before the next
+// are loaded), 47 for the gradient, which keeps a row ahead (5.7 TB/s; 64 with one row
+// in flight and full-precision exponentials). 64 tokens take 19 us on the device, under
+// the 109 that torch's autograd and the calls take on the host.
 #include "../../include/balance.h"
 #include "moe_internal.cuh"
 

@@ -39,13 +39,16 @@
 // TMEM and returns.
 //
 // What bounds it. Few rows: the weights' stream from HBM; 128 rows of 64 experts,
-// gate/up (K 2048, I 1536): 35 us, 5.3 TB/s of it, about 4 us of them the launch's
-// own latencies. Many rows: the 1000 W power cap and the stages' handshakes; 32768
-// rows: 107 us in short runs (SMs at 1.6 GHz, MMAs in half of the cycles), 127 us
-// in long ones (1.4 GHz). The shared load of the weights took 6% off both; half
-// the tile's rows per SM (pairs), 7%; skipping the weights' loads altogether, as a
-// bound, 20%. One row tile's shape, 192 rows: two accumulators and the scales fill
-// TMEM (512 columns).
+// gate/up (K 2048, I 1536), three sets of weights in turn: 35 us, 81% of what a copy
+// reaches, about 4 us of them the launch's own latencies. Many rows: waits between the
+// roles; 32768 rows: 107 us in short runs, with MMAs in half of the cycles (the MMAs
+// alone would take 52 at that clock). Known of them: the first weights of a run wait
+// for the last row tile of the run before where K fills the ring (K 2048; without the
+// weights' loads, as a bound, 20% less), pairs get equal numbers of items and not
+// equal work, and above K 2048 nothing is shared. The 1000 W power cap comes on top:
+// 127 us in long runs (SMs at 1.4 GHz instead of 1.6). The shared load of the weights
+// took 6% off both; half the tile's rows per SM (pairs), 7%. One row tile's shape, 192
+// rows: two accumulators and the scales fill TMEM (512 columns).
 #include <cooperative_groups.h>
 #include <stddef.h>
 
