@@ -92,3 +92,28 @@ def test_outputs_dropped():
     torch.cuda.current_stream().synchronize()
     s.synchronize()
     assert all((t == 99).all() for t in keep)
+
+
+def test_on_a_forked_stream_of_a_capture():
+    """quantize and matmul on a stream that joins the capture; their tensors may go
+    once it is captured, and the next eager calls are not disturbed."""
+    x, w = data(6), mx.quantize(data(7)[:N].contiguous())
+    want = mx.matmul(mx.quantize(x), w)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        s.wait_stream(main)
+        q = mx.quantize(x, stream=s)
+        y = mx.matmul(q, w, stream=s)
+        del q
+        main.wait_stream(s)
+    for seed in (6, 8):
+        x.copy_(data(seed))
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) == (seed == 6)
+        assert torch.equal(y, mx.matmul(mx.quantize(x), w))
+    del g, y
+    assert torch.equal(mx.matmul(mx.quantize(data(6)), w), want) and mx.status() == 0
